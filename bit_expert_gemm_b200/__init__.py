@@ -1,5 +1,6 @@
 """Routed-expert MoE layer (router + top-k, permutation, grouped SwiGLU
-experts in BF16 / AWQ W4A16 g32 / NVFP4 W4A4, combine) and RAZOR Refill-RMS
+experts in BF16 / AWQ W4A16 g32 / NVFP4 W4A4 / FP8 with a scale per block of
+128, combine) and RAZOR Refill-RMS
 expert scoring for NVIDIA B200 (sm_100a).
 
 The compute path is the C ABI of libmoe_b200.so (include/moe.h), bound
@@ -12,8 +13,11 @@ from .abi import (  # noqa: F401
     moe_awq_dequant_g32,
     moe_combine,
     moe_device_status,
+    moe_fp8_quantize_b128,
+    moe_grouped_gemm_fp8_b128,
     moe_grouped_swiglu_awq_g32,
     moe_grouped_swiglu_bf16,
+    moe_grouped_swiglu_fp8_b128,
     moe_grouped_swiglu_nvfp4,
     moe_nvfp4_quantize,
     moe_permute,

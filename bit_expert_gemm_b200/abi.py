@@ -27,7 +27,8 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
                 4: "MOE_ERR_CUDA", 5: "MOE_ERR_TIMEOUT"}
 MOE_DTYPE_BF16, MOE_DTYPE_F16 = 0, 1
 (MOE_OP_ROUTE_TOPK, MOE_OP_PERMUTE, MOE_OP_SWIGLU_BF16, MOE_OP_SWIGLU_AWQ_G32, MOE_OP_SWIGLU_NVFP4, MOE_OP_REFILL,
- MOE_OP_NVFP4_QUANTIZE, MOE_OP_EXPERTS_BF16, MOE_OP_ROUTE_PERMUTE, MOE_OP_EXPERTS_AWQ_G32) = range(10)
+ MOE_OP_NVFP4_QUANTIZE, MOE_OP_EXPERTS_BF16, MOE_OP_ROUTE_PERMUTE, MOE_OP_EXPERTS_AWQ_G32, MOE_OP_SWIGLU_FP8_B128,
+ MOE_OP_LAYER_DECODE) = range(12)
 
 
 class MoEError(RuntimeError):
@@ -71,6 +72,9 @@ _SIGS = {
     "moe_nvfp4_prepack_sf": (_I, [_P, _I, _I, _I, _I, _P, _SZ, _P]),
     "moe_grouped_swiglu_nvfp4_prepacked": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I,
                                                 _P, _P, _SZ, _P]),
+    "moe_fp8_quantize_b128": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_grouped_gemm_fp8_b128": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _I, _I, _P, _P]),
+    "moe_grouped_swiglu_fp8_b128": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _P, _P, _SZ, _P]),
     "moe_combine": (_I, [_P, _I, _P, _I, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "razor_refill_rms_accumulate": (_I, [_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _SZ, _P]),
     "razor_select": (_I, [_P, _P, _I, _I, _P, _P, _P, _P]),
@@ -513,6 +517,125 @@ def moe_grouped_swiglu_nvfp4_prepacked(x, row_token, expert_offsets, rows: int, 
     _call("moe_grouped_swiglu_nvfp4_prepacked", _p(x), _p(row_token), _p(expert_offsets), T, rows, H, I, E,
           _p(w_gu), _p(sf_gu_packed), _p(gs_gu), _p(w_d), _p(sf_d_packed), _p(gs_d), _p(act_gs_in),
           _p(act_gs_out), int(out_fp32), _p(f), _p(ws), ws.numel(), _stream(stream))
+    return f
+
+
+def _same_device(x: torch.Tensor, *others: Optional[torch.Tensor]):
+    """All operands on x's device, and that device current: the library
+    launches on the current device."""
+    for t in others:
+        if t is not None and t.device != x.device:
+            raise ValueError(f"operands on {x.device} and {t.device}")
+    if x.is_cuda and x.device.index != torch.cuda.current_device():
+        raise ValueError(f"operands are on {x.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _fp8_codes(t: torch.Tensor, name: str):
+    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError(f"{name}: expected float8_e4m3fn (or uint8) codes, got {t.dtype}")
+
+
+def _fp8_shape(t: torch.Tensor, shape, name: str):
+    _need(t, torch.float32, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def moe_fp8_quantize_b128(v, block_rows: int = 1, codes=None, scales=None, stream=None):
+    """v [batch, rows, K] (or [rows, K]) 16-bit -> (codes, v's shape, E4M3;
+    scales [.., ceil(rows/block_rows), ceil(K/128)] FP32): one scale per row
+    and 128 columns (block_rows = 1, activations) or per 128 x 128 block
+    (block_rows = 128, weights)."""
+    if v.dim() not in (2, 3):
+        raise ValueError("moe_fp8_quantize_b128: v must be [rows, K] or [batch, rows, K]")
+    R, K = v.shape[-2:]
+    if codes is None:
+        codes = torch.empty(v.shape, dtype=torch.float8_e4m3fn, device=v.device)
+    sshape = (*v.shape[:-2], (R + block_rows - 1) // max(1, block_rows), _blocks(K))
+    if scales is None:
+        scales = torch.empty(sshape, dtype=torch.float32, device=v.device)
+    _fp8_codes(codes, "codes")
+    _fp8_shape(scales, sshape, "scales")
+    if codes.shape != v.shape:
+        raise ValueError("moe_fp8_quantize_b128: codes must have v's shape")
+    _same_device(v, codes, scales)
+    _call("moe_fp8_quantize_b128", _p(v), v.shape[0] if v.dim() == 3 else 1, R, K, block_rows, _dtype_code(v),
+          _p(codes), _p(scales), _stream(stream))
+    return codes, scales
+
+
+def moe_grouped_gemm_fp8_b128(a, a_scales, w, w_scales, expert_offsets=None, row_token=None,
+                              out_dtype=torch.bfloat16, out=None, stream=None):
+    """out [rows, N] = the grouped product of a [T, K] (rows in order, or
+    gathered through row_token [rows]) and w [E, N, K], both E4M3 with a scale
+    per block of 128 (a_scales [T, K/128], w_scales [E, N/128, K/128], rounded
+    up).  expert_offsets [E + 1] may be None for E = 1."""
+    T, K = a.shape
+    E, N, Kw = w.shape
+    if Kw != K:
+        raise ValueError(f"moe_grouped_gemm_fp8_b128: a has K={K}, w has K={Kw}")
+    _fp8_codes(a, "a")
+    _fp8_codes(w, "w")
+    _fp8_shape(a_scales, (T, _blocks(K)), "a_scales")
+    _fp8_shape(w_scales, (E, _blocks(N), _blocks(K)), "w_scales")
+    rows = T
+    if row_token is not None:
+        _need(row_token, torch.int32, "row_token")
+        rows = row_token.numel()
+    if expert_offsets is not None:
+        _need(expert_offsets, torch.int32, "expert_offsets")
+        if expert_offsets.numel() != E + 1:
+            raise ValueError(f"expert_offsets: expected {E + 1} entries, got {expert_offsets.numel()}")
+    if out is None:
+        out = torch.empty((rows, N), dtype=out_dtype, device=a.device)
+    if tuple(out.shape) != (rows, N):
+        raise ValueError(f"out: expected shape {(rows, N)}, got {tuple(out.shape)}")
+    _same_device(a, a_scales, w, w_scales, expert_offsets, row_token, out)
+    fp32 = out.dtype == torch.float32
+    _call("moe_grouped_gemm_fp8_b128", _p(a), _p(a_scales), _p(row_token), _p(expert_offsets), T, rows, K, N, E, _p(w),
+          _p(w_scales), MOE_DTYPE_BF16 if fp32 else _dtype_code(out), int(fp32), _p(out), _stream(stream))
+    return out
+
+
+def _fp8_experts(H: int, E: int, I: int, w_gu, sc_gu, w_d, sc_d):
+    _fp8_codes(w_gu, "w_gu")
+    _fp8_codes(w_d, "w_d")
+    if tuple(w_gu.shape) != (E, 2 * I, H) or tuple(w_d.shape) != (E, H, I):
+        raise ValueError(f"FP8 experts: w_gu must be [E, 2I, H] and w_d [E, H, I], got {tuple(w_gu.shape)} and "
+                         f"{tuple(w_d.shape)} for H={H}")
+    _fp8_shape(sc_gu, (E, 2, _blocks(I), _blocks(H)), "sc_gu")
+    _fp8_shape(sc_d, (E, _blocks(H), _blocks(I)), "sc_d")
+
+
+def moe_grouped_swiglu_fp8_b128(x, row_token, expert_offsets, rows: int, w_gu, sc_gu, w_d, sc_d,
+                                out_fp32: bool = False, f=None, ws=None, stream=None):
+    """Routed experts with FP8 weights (E4M3 codes w_gu [E, 2I, H], w_d [E, H,
+    I]; scales sc_gu [E, 2, I/128, H/128], sc_d [E, H/128, I/128], rounded
+    up): x is quantised per token and 128 features, h per row and 128."""
+    T, H = x.shape
+    E, I = w_gu.shape[0], w_gu.shape[1] // 2
+    dev = x.device
+    _fp8_experts(H, E, I, w_gu, sc_gu, w_d, sc_d)
+    _need(expert_offsets, torch.int32, "expert_offsets")
+    if expert_offsets.numel() != E + 1:
+        raise ValueError(f"expert_offsets: expected {E + 1} entries, got {expert_offsets.numel()}")
+    if row_token is not None:
+        _need(row_token, torch.int32, "row_token")
+        if row_token.numel() < rows:
+            raise ValueError(f"row_token: {row_token.numel()} entries for {rows} rows")
+    if f is None:
+        f = torch.empty((rows, H), dtype=torch.float32 if out_fp32 else x.dtype, device=dev)
+    if tuple(f.shape) != (rows, H) or f.dtype != (torch.float32 if out_fp32 else x.dtype):
+        raise ValueError(f"f: expected [{rows}, {H}] of {'float32' if out_fp32 else x.dtype}")
+    if ws is None:
+        ws = workspace(MOE_OP_SWIGLU_FP8_B128, T, H, E, max(1, -(-rows // max(T, 1))), I, dev)
+    _same_device(x, row_token, expert_offsets, w_gu, sc_gu, w_d, sc_d, f, ws)
+    _call("moe_grouped_swiglu_fp8_b128", _p(x), _p(row_token), _p(expert_offsets), T, rows, H, I, E, _p(w_gu),
+          _p(sc_gu), _p(w_d), _p(sc_d), _dtype_code(x), int(out_fp32), _p(f), _p(ws), ws.numel(), _stream(stream))
     return f
 
 

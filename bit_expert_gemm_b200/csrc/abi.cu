@@ -67,6 +67,15 @@ int grouped_swiglu_nvfp4(const void* x, const int32_t* row_token, const int32_t*
 size_t nvfp4_packed_sf_bytes(int E, int rows_per_expert, int K, int swiglu);
 int nvfp4_prepack_sf(const uint8_t* sf, int E, int rows_per_expert, int K, int swiglu, uint8_t* out,
                      cudaStream_t stream);
+int fp8_quantize(const void* v, int batch, int rows, int K, int block_rows, int dtype, uint8_t* codes, float* scales,
+                 cudaStream_t stream);
+int grouped_gemm_fp8(const uint8_t* a, const float* a_scales, int a_rows, const int32_t* row_token,
+                     const int32_t* offsets, int rows, int K, int N, int E, const uint8_t* w, const float* w_scales,
+                     int out_kind, void* out, cudaStream_t stream);
+size_t fp8_swiglu_ws_bytes(int T, int rows, int H, int I);
+int grouped_swiglu_fp8(const void* x, const int32_t* row_token, const int32_t* offsets, int T, int rows, int H, int I,
+                       int E, const uint8_t* w_gu, const float* sc_gu, const uint8_t* w_d, const float* sc_d,
+                       int dtype, int out_fp32, void* f, void* ws, size_t ws_bytes, cudaStream_t stream);
 int shared_gate(const void* x, int T, int H, const void* w_gate, int dtype, float* gate, cudaStream_t stream);
 int rmsnorm(const void* x, int T, int H, const void* w, float eps, int dtype, void* y, cudaStream_t stream,
             const void* w_gate = nullptr, float* gate = nullptr);
@@ -320,6 +329,7 @@ size_t moe_workspace_size(int op, int T, int H, int E, int k_slots, int I) {
     case MOE_OP_SWIGLU_NVFP4: return nvfp4_ws_bytes(rows, H, I, E);
     case MOE_OP_REFILL: return refill_ws_bytes(T, k_slots > 0 ? k_slots - 1 : 0);
     case MOE_OP_NVFP4_QUANTIZE: return nvfp4_quant_ws_bytes(1, T, H);
+    case MOE_OP_SWIGLU_FP8_B128: return fp8_swiglu_ws_bytes(T, rows, H, I);
     default: return 0;
   }
 }
@@ -631,6 +641,70 @@ int moe_grouped_swiglu_nvfp4_prepacked(const void* x, const int32_t* row_token, 
   return grouped_swiglu_nvfp4(x, row_token, expert_offsets, T, rows, H, I, E, w_gu, nullptr, gs_gu, w_d, nullptr, gs_d,
                               act_gs_in, act_gs_out, out_fp32, f, ws, ws_bytes, static_cast<cudaStream_t>(stream),
                               sf_gu_packed, sf_d_packed);
+}
+
+int moe_fp8_quantize_b128(const void* v, int batch, int rows, int K, int block_rows, int dtype, uint8_t* codes,
+                          float* scales, void* stream) {
+  MOE_REQUIRE(batch >= 0 && rows >= 0 && K >= 0, MOE_ERR_INVALID_ARG, "moe_fp8_quantize_b128: bad sizes");
+  MOE_REQUIRE(dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F16, MOE_ERR_INVALID_ARG, "moe_fp8_quantize_b128: dtype %d",
+              dtype);
+  MOE_REQUIRE(block_rows == 1 || block_rows == 128, MOE_ERR_UNSUPPORTED,
+              "moe_fp8_quantize_b128: block_rows=%d (1 or 128)", block_rows);
+  MOE_REQUIRE(K % 16 == 0, MOE_ERR_UNSUPPORTED, "moe_fp8_quantize_b128: K=%d is not a multiple of 16", K);
+  if (batch == 0 || rows == 0 || K == 0) return MOE_OK;
+  MOE_REQUIRE(v && codes && scales, MOE_ERR_INVALID_ARG, "moe_fp8_quantize_b128: null pointer");
+  MOE_REQUIRE(aligned16(v) && aligned16(codes), MOE_ERR_INVALID_ARG,
+              "moe_fp8_quantize_b128: v / codes not 16-byte aligned");
+  return fp8_quantize(v, batch, rows, K, block_rows, dtype, codes, scales, static_cast<cudaStream_t>(stream));
+}
+
+int moe_grouped_gemm_fp8_b128(const uint8_t* a, const float* a_scales, const int32_t* row_token,
+                              const int32_t* expert_offsets, int T, int rows, int K, int N, int E, const uint8_t* w,
+                              const float* w_scales, int dtype, int out_fp32, void* out, void* stream) {
+  MOE_REQUIRE(T >= 0 && rows >= 0 && K > 0 && N > 0 && E >= 1, MOE_ERR_INVALID_ARG,
+              "moe_grouped_gemm_fp8_b128: bad sizes T=%d rows=%d K=%d N=%d E=%d", T, rows, K, N, E);
+  MOE_REQUIRE(dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F16, MOE_ERR_INVALID_ARG,
+              "moe_grouped_gemm_fp8_b128: dtype %d", dtype);
+  MOE_REQUIRE(K % 16 == 0 && N % 16 == 0, MOE_ERR_UNSUPPORTED,
+              "moe_grouped_gemm_fp8_b128: K=%d and N=%d must be multiples of 16", K, N);
+  MOE_REQUIRE(E <= kGemmMaxGroups && (long long)E * N <= 0x7fffffffLL, MOE_ERR_UNSUPPORTED,
+              "moe_grouped_gemm_fp8_b128: E=%d N=%d", E, N);
+  MOE_REQUIRE(expert_offsets || E == 1, MOE_ERR_INVALID_ARG,
+              "moe_grouped_gemm_fp8_b128: without expert_offsets E (%d) must be 1", E);
+  MOE_REQUIRE(row_token || rows == T, MOE_ERR_INVALID_ARG,
+              "moe_grouped_gemm_fp8_b128: without row_token, rows (%d) must equal T (%d)", rows, T);
+  if (rows == 0) return MOE_OK;
+  MOE_REQUIRE(T > 0, MOE_ERR_INVALID_ARG, "moe_grouped_gemm_fp8_b128: rows without tokens");
+  MOE_REQUIRE(a && a_scales && w && w_scales && out, MOE_ERR_INVALID_ARG, "moe_grouped_gemm_fp8_b128: null pointer");
+  MOE_REQUIRE(aligned16(a) && aligned16(w) && aligned16(out), MOE_ERR_INVALID_ARG,
+              "moe_grouped_gemm_fp8_b128: operands must be 16-byte aligned");
+  return grouped_gemm_fp8(a, a_scales, T, row_token, expert_offsets, rows, K, N, E, w, w_scales,
+                          out_fp32 ? 2 : (dtype == MOE_DTYPE_BF16 ? 0 : 1), out, static_cast<cudaStream_t>(stream));
+}
+
+int moe_grouped_swiglu_fp8_b128(const void* x, const int32_t* row_token, const int32_t* expert_offsets, int T,
+                                int rows, int H, int I, int E, const uint8_t* w_gu, const float* sc_gu,
+                                const uint8_t* w_d, const float* sc_d, int dtype, int out_fp32, void* f, void* ws,
+                                size_t ws_bytes, void* stream) {
+  MOE_REQUIRE(T >= 0 && rows >= 0 && E >= 1, MOE_ERR_INVALID_ARG, "moe_grouped_swiglu_fp8_b128: bad sizes");
+  MOE_REQUIRE(dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F16, MOE_ERR_INVALID_ARG,
+              "moe_grouped_swiglu_fp8_b128: dtype %d", dtype);
+  MOE_REQUIRE(H > 0 && I > 0 && H % 64 == 0 && I % 64 == 0, MOE_ERR_UNSUPPORTED,
+              "moe_grouped_swiglu_fp8_b128: H=%d and I=%d must be positive multiples of 64", H, I);
+  MOE_REQUIRE(E <= kGemmMaxGroups && (long long)E * H <= 0x7fffffffLL && (long long)E * 2 * I <= 0x7fffffffLL,
+              MOE_ERR_UNSUPPORTED, "moe_grouped_swiglu_fp8_b128: E=%d H=%d I=%d", E, H, I);
+  MOE_REQUIRE(row_token || rows == T, MOE_ERR_INVALID_ARG,
+              "moe_grouped_swiglu_fp8_b128: without row_token, rows (%d) must equal T (%d)", rows, T);
+  if (rows == 0) return MOE_OK;
+  MOE_REQUIRE(T > 0, MOE_ERR_INVALID_ARG, "moe_grouped_swiglu_fp8_b128: rows without tokens");
+  MOE_REQUIRE(x && expert_offsets && w_gu && sc_gu && w_d && sc_d && f && ws, MOE_ERR_INVALID_ARG,
+              "moe_grouped_swiglu_fp8_b128: null pointer");
+  MOE_REQUIRE(aligned16(x) && aligned16(w_gu) && aligned16(w_d) && aligned16(f), MOE_ERR_INVALID_ARG,
+              "moe_grouped_swiglu_fp8_b128: operands must be 16-byte aligned");
+  MOE_REQUIRE((reinterpret_cast<uintptr_t>(ws) & 255) == 0, MOE_ERR_WORKSPACE,
+              "moe_grouped_swiglu_fp8_b128: workspace not 256-byte aligned");
+  return grouped_swiglu_fp8(x, row_token, expert_offsets, T, rows, H, I, E, w_gu, sc_gu, w_d, sc_d, dtype, out_fp32, f,
+                            ws, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
 int moe_combine(const void* f, int f_fp32, const int32_t* slot_row, int k_slots, const float* topk_w,

@@ -1,0 +1,533 @@
+// Persistent grouped GEMM on FP8 E4M3 operands with one FP32 scale per block
+// of 128 along K (tcgen05.mma kind::f8f6f4, FP32 accumulate), and the expert
+// FFN made of it.
+//
+//   out[r, n] = sum_kb sa[row(r), kb] * sw[g, n / 128, kb] * P_kb[r, n],
+//   P_kb[r, n] = sum_{k in block kb} e4m3(A[row(r), k]) * e4m3(W[g, n, k])
+//
+// The scales are arbitrary FP32 numbers that change with every K block, so
+// the tensor core's accumulator holds one block only: each K step of 128
+// (one 128-byte swizzle row, four MMAs) starts a fresh accumulator in a ring
+// of TMEM buffers, and eight promotion warps read it, multiply by the two
+// scales and add into FP32 registers.  Per step of a 128 x 256 tile that is
+// 128 FMAs for each of 256 threads against 4 MMAs of M = 128, N = 256, so the
+// two run side by side.
+//
+// SwiGLU form: the tile holds 128 gate and the matching 128 up columns, which
+// is one quantisation block of h per row: the epilogue forms h in FP32, takes
+// the row's maximum (exchanged between the two warps that hold the row's
+// halves) and writes E4M3 codes and the scale; h never goes to memory in 16
+// bits.
+//
+// With row_token, A rows are gathered by four warps with cp.async straight
+// into the 128-byte-swizzled A tile; rows past the group read zero.
+//
+// Warp roles: 0 TMA producer, 1 UMMA issuer (TMEM owner), 2 and 3 idle (they
+// complete a register-allocation group), 4..7 A-row gather, 8..15 promotion
+// and epilogue (two per 32 rows, each half of the tile's columns).
+#include "fp8.cuh"
+#include "gemm_sm100.cuh"
+
+namespace moe {
+
+int make_tmap_2d_u8_sw128(CUtensorMap* map, const void* base, int rows, int cols_bytes, int box_rows);
+int fp8_quantize(const void* v, int batch, int rows, int K, int block_rows, int dtype, uint8_t* codes, float* scales,
+                 cudaStream_t stream);
+
+namespace {
+
+constexpr int BM = 128;
+constexpr int BK = kFp8Block;  // elements = bytes per row and K step
+constexpr int A_BYTES = BM * BK;
+constexpr int kThreads = 512;
+constexpr int kGatherWarp0 = 4;
+constexpr int kEpiWarp0 = 8;
+constexpr int kSmemBudget = 200 * 1024;
+// registers per thread of the role groups: the sum over the four groups of
+// 128 threads is what the block is launched with (512 x 128)
+constexpr int kRegsIssue = 64, kRegsGather = 64, kRegsEpi = 192;
+static_assert(kRegsIssue + kRegsGather + 2 * kRegsEpi == 4 * 128, "register split must equal the launch's total");
+
+template <int BN>
+struct Cfg {
+  static constexpr int B_BYTES = BN * BK;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGES = kSmemBudget / STAGE_BYTES > 8 ? 8 : kSmemBudget / STAGE_BYTES;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+  static constexpr int NACC = 512 / BN;  // TMEM accumulator ring
+  static_assert(STAGE_BYTES % 1024 == 0, "stage must keep 1024-byte alignment");
+};
+
+struct Args {
+  const int* group_offsets;  // [G+1] on the device, or null: one group of `rows` rows
+  int G, rows, K, n_out, b_rows_per_group, up_offset;
+  const float* sa;           // [a_rows, KB]
+  const float* sw;           // [G, w_blocks, KB] (SwiGLU: [G, 2, w_blocks, KB])
+  int w_blocks;
+  void* out;                 // SwiGLU: E4M3 codes of h [rows, n_out]
+  float* out_scales;         // SwiGLU: [rows, w_blocks]
+  int out_kind;              // 0 BF16, 1 FP16, 2 FP32
+  const int32_t* row_token;
+  const uint8_t* a_src;      // [a_rows, K] codes
+  int a_rows;
+  int* status;
+  unsigned long long limit_ns;
+};
+
+// kind::f8f6f4: D FP32, A and B E4M3 (0), K-major, M = 128
+__host__ __device__ constexpr uint32_t idesc_e4m3(int N) {
+  return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(BM >> 4) << 24);
+}
+__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+template <int R>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+struct TileMap {
+  int g, m, n;
+};
+
+// Exclusive scan of the groups' row-tile counts into tile_start[0..G], row
+// offsets into goff[0..G].
+__device__ void build_tile_table(const Args& a, int* goff, int* tile_start, int* warp_sums) {
+  const int G = a.G, tid = threadIdx.x;
+  for (int i = tid; i <= G; i += kThreads) goff[i] = a.group_offsets ? a.group_offsets[i] : (i == 0 ? 0 : a.rows);
+  __syncthreads();
+  const int per = (G + kThreads - 1) / kThreads;
+  const int g0 = tid * per;
+  int local = 0;
+  for (int g = g0; g < g0 + per && g < G; ++g) {
+    const int n = goff[g + 1] - goff[g];
+    local += n > 0 ? (n + BM - 1) / BM : 0;
+  }
+  const int lane = tid & 31, warp = tid >> 5;
+  int incl = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  int run = incl - local;
+  for (int w = 0; w < warp; ++w) run += warp_sums[w];
+  for (int g = g0; g < g0 + per && g < G; ++g) {
+    tile_start[g] = run;
+    const int n = goff[g + 1] - goff[g];
+    run += n > 0 ? (n + BM - 1) / BM : 0;
+  }
+  if (tid == kThreads - 1) tile_start[G] = run;
+  __syncthreads();
+}
+
+__device__ __forceinline__ TileMap decode_tile(int L, int nt, const int* tile_start, int G) {
+  TileMap t;
+  const int mt = L / nt;
+  t.n = L - mt * nt;
+  int lo = 0, hi = G - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tile_start[mid] <= mt) lo = mid; else hi = mid - 1;
+  }
+  t.g = lo;
+  t.m = mt - tile_start[lo];
+  return t;
+}
+
+template <int BN, bool SWIGLU>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_grouped_gemm_fp8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const Args args) {
+  using C = Cfg<BN>;
+  constexpr int STAGES = C::STAGES, NACC = C::NACC;
+  constexpr int BNH = SWIGLU ? BN / 2 : BN;  // output columns per tile
+  constexpr int NC = BN / 2;                 // accumulator columns per promotion thread
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES], tfull_bar[NACC], tempty_bar[NACC], xbar[4],
+      drain_bar;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ volatile int abort_flag;
+  __shared__ int goff[kGemmMaxGroups + 1];
+  __shared__ int tile_start[kGemmMaxGroups + 1];
+  __shared__ int warp_sums[kThreads / 32];
+  __shared__ float row_max[2][2][BM];
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  auto stg = [&](int s) { return smem + s * C::STAGE_BYTES; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool gathered = args.row_token != nullptr;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full_bar[s], 1 + (gathered ? 128 : 0));
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int i = 0; i < NACC; ++i) {
+      mbar_init(&tfull_bar[i], 1);
+      mbar_init(&tempty_bar[i], 8);  // one arrival per promotion warp
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&xbar[i], 2);  // the two warps of a row quadrant
+    mbar_init(&drain_bar, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_base_sh, 512);
+    tmem_relinquish();
+  }
+  build_tile_table(args, goff, tile_start, warp_sums);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_base_sh;
+
+  const int G = args.G;
+  const int nt = (args.n_out + BNH - 1) / BNH;
+  const int total = tile_start[G] * nt;
+  const int KB = fp8_blocks(args.K);
+  int* status = args.status;
+  const unsigned long long lim = args.limit_ns;
+
+  if (warp < kGatherWarp0) {
+    regs_dec<kRegsIssue>();
+    if (warp == 0 && lane == 0) {
+      // ---------------- TMA producer ----------------
+      int stage = 0;
+      uint32_t phase = 0;
+      long issued = 0;
+      bool ok = true;
+      for (int L = blockIdx.x; L < total && ok; L += gridDim.x) {
+        const TileMap t = decode_tile(L, nt, tile_start, G);
+        const int a_row = goff[t.g] + t.m * BM;
+        const int b_row = t.g * args.b_rows_per_group + t.n * BNH;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1, &abort_flag, status, lim)) { ok = false; break; }
+          mbar_arrive_expect_tx(&full_bar[stage], (gathered ? 0 : A_BYTES) + C::B_BYTES);
+          if (!gathered) tma_load_2d(stg(stage), &tmA, &full_bar[stage], kb * BK, a_row);
+          tma_load_2d(stg(stage) + A_BYTES, &tmB, &full_bar[stage], kb * BK, b_row);
+          if (SWIGLU)
+            tma_load_2d(stg(stage) + A_BYTES + BNH * BK, &tmB, &full_bar[stage], kb * BK, b_row + args.up_offset);
+          ++issued;
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        }
+      }
+      if (!ok) {
+        volatile int never = 0;
+        for (long i = (issued > STAGES ? issued - STAGES : 0); i < issued; ++i)
+          mbar_wait(&full_bar[i % STAGES], uint32_t((i / STAGES) & 1), &never, nullptr, lim);
+      }
+    } else if (warp == 1 && lane == 0) {
+      // ---------------- UMMA issuer ----------------
+      constexpr uint32_t idesc = idesc_e4m3(BN);
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, buf_phase = 0;
+      bool ok = true;
+      for (int L = blockIdx.x; L < total && ok; L += gridDim.x) {
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait(&tempty_bar[buf], buf_phase ^ 1, &abort_flag, status, lim) ||
+              !mbar_wait(&full_bar[stage], phase, &abort_flag, status, lim)) {
+            ok = false;
+            break;
+          }
+          if (gathered) fence_proxy_async_smem();  // the gathered rows were written through the generic proxy
+          tc_fence_after();
+          const uint32_t sbase = smem_u32(stg(stage));
+          const uint64_t ad = sdesc_kmajor_sw128(sbase), bd = sdesc_kmajor_sw128(sbase + A_BYTES);
+          const uint32_t d = tmem_base + uint32_t(buf * BN);
+#pragma unroll
+          for (int j = 0; j < BK / 32; ++j)  // K = 32 per MMA: 32 bytes along the swizzled row
+            umma_f8(d, ad + uint64_t(2 * j), bd + uint64_t(2 * j), idesc, j != 0);
+          umma_commit(&empty_bar[stage]);
+          umma_commit(&tfull_bar[buf]);
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+          if (++buf == NACC) { buf = 0; buf_phase ^= 1; }
+        }
+      }
+      umma_commit(&drain_bar);
+      volatile int never = 0;
+      mbar_wait(&drain_bar, 0, &never, nullptr, lim);
+    }
+  } else if (warp < kEpiWarp0) {
+    regs_dec<kRegsGather>();
+    if (gathered) {
+      // ---------------- A row gather ----------------
+      // Thread gt copies 16-byte chunk (gt % 8) of tile rows gt/8, gt/8 + 16, ...
+      const int gt = threadIdx.x - kGatherWarp0 * 32;
+      const int chunk = gt & 7, rbase = gt >> 3;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int L = blockIdx.x; L < total && ok; L += gridDim.x) {
+        const TileMap t = decode_tile(L, nt, tile_start, G);
+        const int a_row = goff[t.g] + t.m * BM;
+        const int g_end = goff[t.g + 1];
+        int tok[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = a_row + rbase + 16 * i;
+          const int tk = (r < g_end && r < args.rows) ? __ldg(args.row_token + r) : -1;
+          tok[i] = (tk >= 0 && tk < args.a_rows) ? tk : -1;
+        }
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1, &abort_flag, status, lim)) { ok = false; break; }
+          const uint32_t dst0 = smem_u32(stg(stage));
+          const int k0 = kb * BK + chunk * 16;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = rbase + 16 * i;
+            const uint32_t dst = dst0 + uint32_t(r * 128 + ((chunk ^ (r & 7)) << 4));
+            const bool v = tok[i] >= 0 && k0 < args.K;
+            cp_async_16_zfill(dst, args.a_src + (v ? size_t(tok[i]) * args.K + k0 : 0), v ? 16u : 0u);
+          }
+          cp_async_arrive_noinc(&full_bar[stage]);
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");  // every copy has landed before the CTA exits
+    }
+  } else {
+    regs_inc<kRegsEpi>();
+    // ---------------- promotion and epilogue ----------------
+    const int q = warp & 3;                   // TMEM lane quadrant: tile rows 32q .. 32q+31
+    const int half = (warp - kEpiWarp0) >> 2; // column half
+    const int row_in_tile = q * 32 + lane;
+    int buf = 0;
+    uint32_t buf_phase = 0, x_phase = 0;
+    bool ok = true;
+    for (int L = blockIdx.x; L < total && ok; L += gridDim.x) {
+      const TileMap t = decode_tile(L, nt, tile_start, G);
+      const int tile_rows = min(BM, min(goff[t.g + 1], args.rows) - (goff[t.g] + t.m * BM));
+      const size_t out_row = size_t(goff[t.g]) + size_t(t.m) * BM + row_in_tile;
+      const bool valid = row_in_tile < tile_rows;
+      // columns of this thread: output columns col0 .. (SwiGLU: BNH/2 of them, gate and up)
+      const int col0 = t.n * BNH + half * (SWIGLU ? BNH / 2 : NC);
+      const bool live = q * 32 < tile_rows && col0 < args.n_out;  // uniform in the warp
+      const float* sa = args.sa;
+      bool row_ok = valid;
+      if (valid) {
+        int src = int(out_row);
+        if (gathered) src = __ldg(args.row_token + out_row);
+        row_ok = src >= 0 && src < args.a_rows;
+        sa += size_t(row_ok ? src : 0) * KB;
+      }
+      const int nb = col0 / kFp8Block;
+      const float* sw0 = args.sw + (SWIGLU ? (size_t(t.g) * 2 * args.w_blocks + nb) : (size_t(t.g) * args.w_blocks + nb)) * KB;
+      const float* sw1 = sw0 + (SWIGLU ? size_t(args.w_blocks) * KB : 0);
+      float acc[NC];
+#pragma unroll
+      for (int i = 0; i < NC; ++i) acc[i] = 0.0f;
+      float na = 0.0f, n0 = 0.0f, n1 = 0.0f;
+      if (live) {
+        na = row_ok ? __ldg(sa) : 0.0f;
+        n0 = __ldg(sw0);
+        n1 = SWIGLU ? __ldg(sw1) : n0;
+      }
+      const uint32_t lane_base = tmem_base + (uint32_t(q * 32) << 16);
+      for (int kb = 0; kb < KB; ++kb) {
+        const float s0 = na * n0, s1 = na * n1;
+        if (live && kb + 1 < KB) {
+          na = row_ok ? __ldg(sa + kb + 1) : 0.0f;
+          n0 = __ldg(sw0 + kb + 1);
+          n1 = SWIGLU ? __ldg(sw1 + kb + 1) : n0;
+        }
+        if (!mbar_wait(&tfull_bar[buf], buf_phase, &abort_flag, status, lim)) { ok = false; break; }
+        tc_fence_after();
+        if (live) {
+#pragma unroll
+          for (int c = 0; c < NC / 32; ++c) {
+            // SwiGLU: the first half of the chunks are gate columns, the rest the matching up columns
+            const int col = SWIGLU ? (c < NC / 64 ? half * (BNH / 2) + 32 * c : BNH + half * (BNH / 2) + 32 * (c - NC / 64))
+                                   : half * NC + 32 * c;
+            const float s = SWIGLU && c >= NC / 64 ? s1 : s0;
+            float v[32];
+            tmem_ld32(lane_base + uint32_t(buf * BN + col), v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(v[i], s, acc[32 * c + i]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+        if (++buf == NACC) { buf = 0; buf_phase ^= 1; }
+      }
+      if (!ok) break;
+      if (SWIGLU) {
+        constexpr int NH = NC / 2;  // h columns of this thread
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NH; ++i) {
+          const float g = acc[i];
+          acc[i] = (g / (1.0f + __expf(-g))) * acc[NH + i];
+          if (col0 + (i & ~31) >= args.n_out) acc[i] = 0.0f;  // n_out is a multiple of 64: whole chunks
+          amax = fmaxf(amax, fabsf(acc[i]));
+        }
+        if (!live) amax = 0.0f;
+        row_max[x_phase][half][row_in_tile] = amax;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&xbar[q]);
+        if (!mbar_wait(&xbar[q], x_phase, &abort_flag, status, lim)) break;
+        amax = fmaxf(amax, row_max[x_phase][half ^ 1][row_in_tile]);
+        x_phase ^= 1;
+        if (live && valid) {
+          const Fp8Scale s = fp8_scale(amax);
+          uint8_t* dst = static_cast<uint8_t*>(args.out) + out_row * args.n_out + col0;
+#pragma unroll
+          for (int i = 0; i < NH / 16; ++i) {
+            uint32_t p[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float* a = acc + 16 * i + 4 * j;
+              p[j] = fp8_quant4(a[0], a[1], a[2], a[3], s.r);
+            }
+            st_global_v4(dst + 16 * i, p[0], p[1], p[2], p[3]);
+          }
+          if (half == 0) args.out_scales[out_row * args.w_blocks + nb] = s.s;
+        }
+      } else if (live && valid) {
+        const size_t at = out_row * args.n_out + col0;
+#pragma unroll
+        for (int i = 0; i < NC / 8; ++i) {
+          if (col0 + 8 * i >= args.n_out) break;
+          const float* a = acc + 8 * i;
+          if (args.out_kind == 2) {
+            float* dst = static_cast<float*>(args.out) + at + 8 * i;
+            st_global_v4(dst, __float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]),
+                         __float_as_uint(a[3]));
+            st_global_v4(dst + 4, __float_as_uint(a[4]), __float_as_uint(a[5]), __float_as_uint(a[6]),
+                         __float_as_uint(a[7]));
+          } else {
+            uint16_t* dst = static_cast<uint16_t*>(args.out) + at + 8 * i;
+            uint32_t p[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              p[j] = args.out_kind == 0 ? Pack2<__nv_bfloat16>::pack(a[2 * j], a[2 * j + 1])
+                                        : Pack2<__half>::pack(a[2 * j], a[2 * j + 1]);
+            st_global_v4(dst, p[0], p[1], p[2], p[3]);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+template <int BN, bool SWIGLU>
+int launch(const Args& a, const uint8_t* w, int w_rows, cudaStream_t stream) {
+  CUtensorMap ta, tb;
+  int rc = make_tmap_2d_u8_sw128(&ta, a.a_src, a.a_rows, a.K, BM);
+  if (rc) return rc;
+  rc = make_tmap_2d_u8_sw128(&tb, w, w_rows, a.K, SWIGLU ? BN / 2 : BN);
+  if (rc) return rc;
+  auto kern = k_grouped_gemm_fp8<BN, SWIGLU>;
+  static bool attr_set[64] = {false};
+  int dev = 0;
+  MOE_CHECK_CUDA(cudaGetDevice(&dev));
+  if (dev >= 64 || !attr_set[dev]) {
+    MOE_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::SMEM_BYTES));
+    if (dev < 64) attr_set[dev] = true;
+  }
+  kern<<<num_sms(), kThreads, Cfg<BN>::SMEM_BYTES, stream>>>(ta, tb, a);
+  MOE_CHECK_CUDA(cudaGetLastError());
+  return MOE_OK;
+}
+
+}  // namespace
+
+// out [rows, N] = the grouped product of a [a_rows, K] and w [E, N, K].
+int grouped_gemm_fp8(const uint8_t* a, const float* a_scales, int a_rows, const int32_t* row_token,
+                     const int32_t* offsets, int rows, int K, int N, int E, const uint8_t* w, const float* w_scales,
+                     int out_kind, void* out, cudaStream_t stream) {
+  Args g{};
+  g.group_offsets = offsets;
+  g.G = E;
+  g.rows = rows;
+  g.K = K;
+  g.n_out = N;
+  g.b_rows_per_group = N;
+  g.sa = a_scales;
+  g.sw = w_scales;
+  g.w_blocks = fp8_blocks(N);
+  g.out = out;
+  g.out_kind = out_kind;
+  g.row_token = row_token;
+  g.a_src = a;
+  g.a_rows = a_rows;
+  g.status = device_status_ptr();
+  g.limit_ns = wait_limit_ns();
+  // the wide tile where an upper bound of its tiles still covers the SMs
+  const long mt = (rows + BM - 1) / BM + (E < rows ? E : rows);
+  if (mt * ((N + 255) / 256) >= num_sms()) return launch<256, false>(g, w, E * N, stream);
+  return launch<128, false>(g, w, E * N, stream);
+}
+
+size_t fp8_swiglu_ws_bytes(int T, int rows, int H, int I) {
+  WsCounter c;
+  c.take<uint8_t>(size_t(T) * H);
+  c.take<float>(size_t(T) * fp8_blocks(H));
+  c.take<uint8_t>(size_t(rows) * I);
+  c.take<float>(size_t(rows) * fp8_blocks(I));
+  return c.used;
+}
+
+int grouped_swiglu_fp8(const void* x, const int32_t* row_token, const int32_t* offsets, int T, int rows, int H, int I,
+                       int E, const uint8_t* w_gu, const float* sc_gu, const uint8_t* w_d, const float* sc_d,
+                       int dtype, int out_fp32, void* f, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  WsCarver carve(ws, ws_bytes);
+  uint8_t* xq = carve.take<uint8_t>(size_t(T) * H);
+  float* xs = carve.take<float>(size_t(T) * fp8_blocks(H));
+  uint8_t* hq = carve.take<uint8_t>(size_t(rows) * I);
+  float* hs = carve.take<float>(size_t(rows) * fp8_blocks(I));
+  MOE_REQUIRE(carve.ok, MOE_ERR_WORKSPACE, "moe_grouped_swiglu_fp8_b128: workspace of %zu bytes is too small (need %zu)",
+              ws_bytes, fp8_swiglu_ws_bytes(T, rows, H, I));
+  int rc = fp8_quantize(x, 1, T, H, 1, dtype, xq, xs, stream);
+  if (rc) return rc;
+  Args g{};
+  g.group_offsets = offsets;
+  g.G = E;
+  g.rows = rows;
+  g.K = H;
+  g.n_out = I;
+  g.b_rows_per_group = 2 * I;
+  g.up_offset = I;
+  g.sa = xs;
+  g.sw = sc_gu;
+  g.w_blocks = fp8_blocks(I);
+  g.out = hq;
+  g.out_scales = hs;
+  g.row_token = row_token;
+  g.a_src = xq;
+  g.a_rows = T;
+  g.status = device_status_ptr();
+  g.limit_ns = wait_limit_ns();
+  rc = launch<256, true>(g, w_gu, E * 2 * I, stream);
+  if (rc) return rc;
+  return grouped_gemm_fp8(hq, hs, rows, nullptr, offsets, rows, I, H, E, w_d, sc_d,
+                          out_fp32 ? 2 : (dtype == MOE_DTYPE_BF16 ? 0 : 1), f, stream);
+}
+
+}  // namespace moe

@@ -4,7 +4,8 @@ MoELayer owns the device weights of one layer plus every intermediate
 buffer and workspace for a maximum token count, so that a forward pass
 launches only the library's kernels (no allocation, no host sync).  The
 weight format is one of "bf16" (16-bit weights, BF16 or FP16 activations),
-"awq_g32" and "nvfp4"; the router and the shared expert are always 16-bit.
+"awq_g32", "nvfp4" and "fp8_b128" (E4M3 with an FP32 scale per block of 128);
+the router and the shared expert are always 16-bit.
 
 forward(x)               x [T, H] on the device -> y [T, H]; with a pre-MoE
                          RMSNorm gain in the weights ("w_norm" [H]) the
@@ -67,6 +68,21 @@ def prepare_nvfp4_weights(w: Dict[str, torch.Tensor]) -> Dict[str, torch.Tensor]
     return out
 
 
+def prepare_fp8_weights(w: Dict[str, torch.Tensor]) -> Dict[str, torch.Tensor]:
+    """Adds FP8 copies of the 16-bit expert weights, quantised by the library
+    (moe_fp8_quantize_b128, one scale per 128 x 128 block): gate, up and down of
+    every expert are separate tensors, whose blocks do not mix.
+    w8_gu [E, 2I, H], sc8_gu [E, 2, I/128, H/128]; w8_d [E, H, I], sc8_d [E,
+    H/128, I/128] (block counts rounded up)."""
+    gu, wd = w["w_gate_up"], w["w_down"]
+    E, I2, H = gu.shape
+    out = dict(w)
+    c, sc = abi.moe_fp8_quantize_b128(gu.reshape(2 * E, I2 // 2, H), block_rows=128)
+    out["w8_gu"], out["sc8_gu"] = c.reshape(E, I2, H), sc.reshape(E, 2, *sc.shape[1:])
+    out["w8_d"], out["sc8_d"] = abi.moe_fp8_quantize_b128(wd, block_rows=128)
+    return out
+
+
 class MoELayer:
     def __init__(self, weights: Dict[str, torch.Tensor], k: int, fmt: str = "bf16", T_max: int = 8192,
                  extra: int = 0, device: Optional[torch.device] = None):
@@ -95,6 +111,10 @@ class MoELayer:
             if "w_gu" not in weights:
                 self.w = weights = prepare_nvfp4_weights(weights)
             self.I = weights["w_gu"].shape[1] // 2
+        elif fmt == "fp8_b128":
+            if "w8_gu" not in weights:
+                self.w = weights = prepare_fp8_weights(weights)
+            self.I = weights["w8_gu"].shape[1] // 2
         else:
             raise ValueError(fmt)
         self._alloc(T_max)
@@ -112,7 +132,7 @@ class MoELayer:
         self.row_token = torch.empty((rows,), dtype=i32, device=d)
         self.slot_row = torch.empty((T_max, ks), dtype=i32, device=d)
         # routed rows f: FP32 for Refill, else the activation dtype (BF16 for NVFP4)
-        f_dt = torch.float32 if self.extra else (self.adt if self.fmt in ("bf16", "awq_g32") else torch.bfloat16)
+        f_dt = torch.float32 if self.extra else (self.adt if self.fmt != "nvfp4" else torch.bfloat16)
         self.f = torch.empty((rows, H), dtype=f_dt, device=d)
         self.shared = torch.empty((T_max, H), dtype=self.adt, device=d)
         # optional shared-expert gate (weights key "w_sh_gate", [H]): sigmoid(x . w) per token
@@ -121,7 +141,7 @@ class MoELayer:
         self.x_norm = torch.empty((T_max, H), dtype=self.adt, device=d) if self.norm else None
         self.y = torch.empty((T_max, H), dtype=self.adt, device=d)
         op = {"bf16": abi.MOE_OP_SWIGLU_BF16, "awq_g32": abi.MOE_OP_SWIGLU_AWQ_G32,
-              "nvfp4": abi.MOE_OP_SWIGLU_NVFP4}[self.fmt]
+              "nvfp4": abi.MOE_OP_SWIGLU_NVFP4, "fp8_b128": abi.MOE_OP_SWIGLU_FP8_B128}[self.fmt]
         # route + permute in one call; the T_max workspace covers every T <= T_max
         self.ws_route = abi.workspace(abi.MOE_OP_ROUTE_PERMUTE, T_max, H, E, ks, 0, d)
         self.ws_ffn = abi.workspace(op, T_max, H, E, ks, self.I, d)
@@ -180,6 +200,10 @@ class MoELayer:
             abi.moe_grouped_swiglu_awq_g32(x, self.row_token[:rows], self.offsets, rows, w["qw_gu"], w["qz_gu"],
                                            w["sc_gu"], w["qw_d"], w["qz_d"], w["sc_d"],
                                            out_fp32=f.dtype == torch.float32, f=f, ws=self.ws_ffn)
+        elif self.fmt == "fp8_b128":
+            abi.moe_grouped_swiglu_fp8_b128(x, self.row_token[:rows], self.offsets, rows, w["w8_gu"], w["sc8_gu"],
+                                            w["w8_d"], w["sc8_d"], out_fp32=f.dtype == torch.float32, f=f,
+                                            ws=self.ws_ffn)
         else:
             abi.moe_grouped_swiglu_nvfp4_prepacked(x, self.row_token[:rows], self.offsets, rows, w["w_gu"],
                                                    w["sfp_gu"], w["gs_gu"], w["w_d"], w["sfp_d"], w["gs_d"],
@@ -305,7 +329,7 @@ class MoELayer:
 # Tensors of a layer whose leading axis (or, for the flat tile-packed copies,
 # whose equal per-expert blocks) belong to one routed expert each.
 EXPERT_TENSORS = ("w_router", "bias", "w_gate_up", "w_down", "qw_gu", "qz_gu", "sc_gu", "qw_d", "qz_d", "sc_d",
-                  "w_gu", "sf_gu", "gs_gu", "w_d", "sf_d", "gs_d")
+                  "w_gu", "sf_gu", "gs_gu", "w_d", "sf_d", "gs_d", "w8_gu", "sc8_gu", "w8_d", "sc8_d")
 EXPERT_PACKED = ("awq_packed", "sfp_gu", "sfp_d")
 
 

@@ -85,7 +85,9 @@ enum {
   MOE_OP_NVFP4_QUANTIZE = 6,
   MOE_OP_EXPERTS_BF16 = 7,
   MOE_OP_ROUTE_PERMUTE = 8,
-  MOE_OP_EXPERTS_AWQ_G32 = 9
+  MOE_OP_EXPERTS_AWQ_G32 = 9,
+  MOE_OP_SWIGLU_FP8_B128 = 10,
+  MOE_OP_LAYER_DECODE = 11
 };
 
 /* Version of this header's ABI. */
@@ -455,6 +457,64 @@ MOE_API int moe_grouped_swiglu_nvfp4_prepacked(const void* x, const int32_t* row
                                                const uint8_t* sf_d_packed, const float* gs_d,
                                                const float* act_gs_in, float* act_gs_out, int out_fp32, void* f,
                                                void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * FP8 E4M3 quantisation with one FP32 scale per block of 128 (the pages have
+ * no FP8 experts; this is the format of block-scaled 8-bit checkpoints).  A
+ * block is block_rows x 128 values: block_rows = 1 for activations (a scale
+ * per row and 128 columns), 128 for weights.  Per block, each step one FP32
+ * IEEE operation rounded to nearest even:
+ *     a = max(amax(|block|), 2^-80),  s = a / 448,  r = 448 / a
+ *     code = e4m3_rn_satfinite(v * r);   the code stands for e4m3(code) * s
+ * v [batch, rows, K] dtype; codes [batch, rows, K] uint8; scales [batch,
+ * ceil(rows/block_rows), ceil(K/128)] FP32 (blocks at the edges are partial).
+ * A block that holds an infinity has s = +inf and decodes as NaN; a NaN has
+ * the E4M3 NaN code and takes no part in the maximum.
+ * Limits: K % 16 == 0; v and codes 16-byte aligned; for block_rows = 128 at
+ * most 2^31 - 1 blocks in one call.
+ * ------------------------------------------------------------------------- */
+MOE_API int moe_fp8_quantize_b128(const void* v, int batch, int rows, int K, int block_rows, int dtype, uint8_t* codes,
+                                  float* scales, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Grouped matrix product of FP8 E4M3 operands with a scale for each block of
+ * 128 (moe_fp8_quantize_b128's formats):
+ *   for every expert e and every row r of e (expert_offsets), i = row_token[r]:
+ *     out[r, n] = sum_kb a_scales[i, kb] * w_scales[e, n/128, kb]
+ *                        * sum_{k in block kb} e4m3(a[i, k]) * e4m3(w[e, n, k])
+ * FP32 sums.  a [T, K] uint8 and a_scales [T, ceil(K/128)]; row_token [rows]
+ * int32, or NULL for the identity (rows must then equal T); expert_offsets
+ * [E+1] int32 on the device, or NULL for one group of all rows (E must then be
+ * 1); w [E, N, K] uint8 and w_scales [E, ceil(N/128), ceil(K/128)]; out [rows,
+ * N], FP32 when out_fp32 != 0, else dtype.  A row whose row_token lies outside
+ * [0, T) is zero; rows from expert_offsets[E] on are left as they were.
+ * Limits: K % 16 == 0, N % 16 == 0, E <= 1024, E * N < 2^31; a, w and out
+ * 16-byte aligned.  No workspace.
+ * ------------------------------------------------------------------------- */
+MOE_API int moe_grouped_gemm_fp8_b128(const uint8_t* a, const float* a_scales, const int32_t* row_token,
+                                      const int32_t* expert_offsets, int T, int rows, int K, int N, int E,
+                                      const uint8_t* w, const float* w_scales, int dtype, int out_fp32, void* out,
+                                      void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Grouped SwiGLU expert FFN [ARCH] with FP8 E4M3 weights and activations and a
+ * scale for each block of 128.  x is quantised per (token, 128 features);
+ * gate and up are moe_grouped_gemm_fp8_b128 products; h = silu(g) * u is formed
+ * in FP32 and quantised per (row, 128 features) from FP32 (it is never rounded
+ * to 16 bits); f is the product of that h and the down projection.
+ *   w_gu [E, 2I, H] uint8 (gate rows, then up rows), sc_gu [E, 2, ceil(I/128),
+ *   ceil(H/128)] FP32 (gate and up are separate tensors: their blocks do not
+ *   mix); w_d [E, H, I], sc_d [E, ceil(H/128), ceil(I/128)].
+ * x [T, H] dtype; row_token [rows] or NULL (rows == T); expert_offsets [E+1];
+ * f [rows, H], FP32 when out_fp32 != 0, else dtype.
+ * Limits: H % 64 == 0, I % 64 == 0, E <= 1024, E * max(2I, H) < 2^31;
+ * operands 16-byte aligned.  Workspace: MOE_OP_SWIGLU_FP8_B128 (the codes and
+ * scales of x and h).
+ * ------------------------------------------------------------------------- */
+MOE_API int moe_grouped_swiglu_fp8_b128(const void* x, const int32_t* row_token, const int32_t* expert_offsets, int T,
+                                        int rows, int H, int I, int E, const uint8_t* w_gu, const float* sc_gu,
+                                        const uint8_t* w_d, const float* sc_d, int dtype, int out_fp32, void* f,
+                                        void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Weighted combine [ARCH]:

@@ -18,6 +18,7 @@ moe      router, softmax + top-k + renormalisation, permutation, SwiGLU expert,
          combine, whole layer.
 awq      AWQ W4A16 asymmetric group-32 pack / unpack / dequantise / quantise.
 nvfp4    NVFP4 W4A4 group-16 quantise / dequantise.
+fp8      FP8 E4M3 with an FP32 scale per block of 128.
 razor    Refill-RMS score (literal definition and brute-force knock-out),
          additive accumulation, expert selection.
 
@@ -25,4 +26,4 @@ Parity status of each function is stated in its docstring; the pins live in
 ``tests/test_oracle_*.py``.
 """
 
-from . import formats, moe, awq, nvfp4, razor  # noqa: F401
+from . import formats, moe, awq, fp8, nvfp4, razor  # noqa: F401
