@@ -19,6 +19,8 @@ from .abi import (  # noqa: F401
     moe_grouped_swiglu_bf16,
     moe_grouped_swiglu_fp8_b128,
     moe_grouped_swiglu_nvfp4,
+    moe_layer_decode_bf16,
+    moe_layer_decode_fp8_b128,
     moe_nvfp4_quantize,
     moe_permute,
     moe_route_topk,

@@ -75,6 +75,10 @@ _SIGS = {
     "moe_fp8_quantize_b128": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P]),
     "moe_grouped_gemm_fp8_b128": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _I, _I, _P, _P]),
     "moe_grouped_swiglu_fp8_b128": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _P, _P, _SZ, _P]),
+    "moe_layer_decode_bf16": (_I, [_P, _I, _I, _P, ctypes.c_float, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _I, _P, _P,
+                                   _P, _P, _SZ, _P]),
+    "moe_layer_decode_fp8_b128": (_I, [_P, _I, _I, _P, ctypes.c_float, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P,
+                                       _I, _P, _P, _P, _P, _SZ, _P]),
     "moe_combine": (_I, [_P, _I, _P, _I, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "razor_refill_rms_accumulate": (_I, [_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _SZ, _P]),
     "razor_select": (_I, [_P, _P, _I, _I, _P, _P, _P, _P]),
@@ -637,6 +641,62 @@ def moe_grouped_swiglu_fp8_b128(x, row_token, expert_offsets, rows: int, w_gu, s
     _call("moe_grouped_swiglu_fp8_b128", _p(x), _p(row_token), _p(expert_offsets), T, rows, H, I, E, _p(w_gu),
           _p(sc_gu), _p(w_d), _p(sc_d), _dtype_code(x), int(out_fp32), _p(f), _p(ws), ws.numel(), _stream(stream))
     return f
+
+
+def _layer_decode(name, x, w_router, bias, k, I, experts, w_sh_gate_up, w_sh_down, norm_w, eps, w_shared_gate,
+                  topk_idx, topk_w, y, ws, stream):
+    T, H = x.shape
+    E = w_router.shape[0]
+
+    def need(t, shape, what, dtype=x.dtype):
+        if t is not None and (t.dtype != dtype or tuple(t.shape) != shape):
+            raise ValueError(f"{name}: {what} must be {list(shape)} of {dtype}, got {list(t.shape)} of {t.dtype}")
+
+    need(w_router, (E, H), "w_router")
+    need(bias, (E,), "bias", torch.float32)
+    need(norm_w, (H,), "norm_w")
+    need(w_shared_gate, (H,), "w_shared_gate")
+    need(w_sh_gate_up, (2 * I, H), "w_sh_gate_up")
+    need(w_sh_down, (H, I), "w_sh_down")
+    need(topk_idx, (T, k), "topk_idx", torch.int32)
+    need(topk_w, (T, k), "topk_w", torch.float32)
+    if y is None:
+        y = torch.empty_like(x)
+    need(y, (T, H), "y")
+    if ws is None:
+        ws = workspace(MOE_OP_LAYER_DECODE, T, H, E, k, I, x.device)
+    _same_device(x, w_router, bias, *experts, w_sh_gate_up, w_sh_down, norm_w, w_shared_gate, topk_idx, topk_w, y, ws)
+    _call(name, _p(x), T, H, _p(norm_w), float(eps), _p(w_shared_gate), _p(w_router), _p(bias), E, k, I,
+          *[_p(t) for t in experts], _p(w_sh_gate_up), _p(w_sh_down), _dtype_code(x), _p(topk_idx), _p(topk_w), _p(y),
+          _p(ws), ws.numel(), _stream(stream))
+    return y
+
+
+def moe_layer_decode_bf16(x, w_router, bias, k: int, w_gate_up, w_down, w_sh_gate_up=None, w_sh_down=None, norm_w=None,
+                          eps: float = 1e-6, w_shared_gate=None, topk_idx=None, topk_w=None, y=None, ws=None,
+                          stream=None):
+    """A whole MoE layer with 16-bit experts on x [T <= 16, H] in one kernel:
+    optional RMSNorm (norm_w), routing, experts, optional shared expert and
+    its gate, weighted sum.  Returns y [T, H]; topk_idx [T, k] int32 and
+    topk_w [T, k] FP32 receive the selection when given."""
+    E, I2, H = w_gate_up.shape
+    if w_gate_up.dtype != x.dtype or w_down.dtype != x.dtype or tuple(w_down.shape) != (E, H, I2 // 2) or \
+            (E, H) != (w_router.shape[0], x.shape[1]):
+        raise ValueError(f"moe_layer_decode_bf16: experts [E, 2I, H] and [E, H, I] of {x.dtype} expected, got "
+                         f"{list(w_gate_up.shape)} and {list(w_down.shape)}")
+    return _layer_decode("moe_layer_decode_bf16", x, w_router, bias, k, I2 // 2, (w_gate_up, w_down), w_sh_gate_up,
+                         w_sh_down, norm_w, eps, w_shared_gate, topk_idx, topk_w, y, ws, stream)
+
+
+def moe_layer_decode_fp8_b128(x, w_router, bias, k: int, w_gu, sc_gu, w_d, sc_d, w_sh_gate_up=None, w_sh_down=None,
+                              norm_w=None, eps: float = 1e-6, w_shared_gate=None, topk_idx=None, topk_w=None, y=None,
+                              ws=None, stream=None):
+    """moe_layer_decode_bf16 with FP8 experts (moe_grouped_swiglu_fp8_b128's
+    weights and scales); router and shared expert in x's dtype."""
+    I = w_gu.shape[1] // 2
+    _fp8_experts(x.shape[1], w_router.shape[0], I, w_gu, sc_gu, w_d, sc_d)
+    return _layer_decode("moe_layer_decode_fp8_b128", x, w_router, bias, k, I, (w_gu, sc_gu, w_d, sc_d), w_sh_gate_up,
+                         w_sh_down, norm_w, eps, w_shared_gate, topk_idx, topk_w, y, ws, stream)
 
 
 def moe_combine(f, slot_row, topk_w, shared_out=None, shared_gate=None, y=None, dtype=None, stream=None):

@@ -76,6 +76,12 @@ size_t fp8_swiglu_ws_bytes(int T, int rows, int H, int I);
 int grouped_swiglu_fp8(const void* x, const int32_t* row_token, const int32_t* offsets, int T, int rows, int H, int I,
                        int E, const uint8_t* w_gu, const float* sc_gu, const uint8_t* w_d, const float* sc_d,
                        int dtype, int out_fp32, void* f, void* ws, size_t ws_bytes, cudaStream_t stream);
+size_t layer_decode_ws_bytes(int T, int E, int k, int I);
+bool layer_decode_fits(int T, int H);
+int layer_decode(const void* x, int T, int H, const void* norm_w, float eps, const void* w_shared_gate,
+                 const void* w_router, const float* bias, int E, int k, int I, const void* w_gu, const float* sc_gu,
+                 const void* w_d, const float* sc_d, bool f8, const void* w_sh_gu, const void* w_sh_d, int dtype,
+                 int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes, cudaStream_t stream);
 int shared_gate(const void* x, int T, int H, const void* w_gate, int dtype, float* gate, cudaStream_t stream);
 int rmsnorm(const void* x, int T, int H, const void* w, float eps, int dtype, void* y, cudaStream_t stream,
             const void* w_gate = nullptr, float* gate = nullptr);
@@ -329,6 +335,7 @@ size_t moe_workspace_size(int op, int T, int H, int E, int k_slots, int I) {
     case MOE_OP_SWIGLU_NVFP4: return nvfp4_ws_bytes(rows, H, I, E);
     case MOE_OP_REFILL: return refill_ws_bytes(T, k_slots > 0 ? k_slots - 1 : 0);
     case MOE_OP_NVFP4_QUANTIZE: return nvfp4_quant_ws_bytes(1, T, H);
+    case MOE_OP_LAYER_DECODE: return layer_decode_fits(T, H) ? layer_decode_ws_bytes(T, E, k_slots, I) : 0;
     case MOE_OP_SWIGLU_FP8_B128: return fp8_swiglu_ws_bytes(T, rows, H, I);
     default: return 0;
   }
@@ -705,6 +712,56 @@ int moe_grouped_swiglu_fp8_b128(const void* x, const int32_t* row_token, const i
               "moe_grouped_swiglu_fp8_b128: workspace not 256-byte aligned");
   return grouped_swiglu_fp8(x, row_token, expert_offsets, T, rows, H, I, E, w_gu, sc_gu, w_d, sc_d, dtype, out_fp32, f,
                             ws, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+static int layer_decode_entry(const char* fn, const void* x, int T, int H, const void* norm_w, float eps,
+                              const void* w_shared_gate, const void* w_router, const float* bias, int E, int k, int I,
+                              const void* w_gu, const float* sc_gu, const void* w_d, const float* sc_d, bool f8,
+                              const void* w_sh_gate_up, const void* w_sh_down, int dtype, int32_t* topk_idx,
+                              float* topk_w, void* y, void* ws, size_t ws_bytes, void* stream) {
+  MOE_REQUIRE(T >= 0 && H > 0 && I > 0 && E >= 1 && k >= 1, MOE_ERR_INVALID_ARG,
+              "%s: bad sizes T=%d H=%d I=%d E=%d k=%d", fn, T, H, I, E, k);
+  MOE_REQUIRE(dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F16, MOE_ERR_INVALID_ARG, "%s: dtype %d", fn, dtype);
+  MOE_REQUIRE(k <= 16 && k <= E && E <= 1024, MOE_ERR_UNSUPPORTED, "%s: need k <= 16, k <= E <= 1024 (k=%d E=%d)", fn, k,
+              E);
+  MOE_REQUIRE(H % 64 == 0 && I % 64 == 0 && I <= 8192 && layer_decode_fits(T, H), MOE_ERR_UNSUPPORTED,
+              "%s: need T <= 16, H %% 64 == 0, H <= 4096, T * H <= 40960, I %% 64 == 0 (T=%d H=%d I=%d)", fn, T, H, I);
+  if (T == 0) return MOE_OK;
+  MOE_REQUIRE(x && w_router && w_gu && w_d && y && ws && (!f8 || (sc_gu && sc_d)), MOE_ERR_INVALID_ARG,
+              "%s: null pointer", fn);
+  MOE_REQUIRE(!w_sh_gate_up == !w_sh_down && (w_sh_gate_up || !w_shared_gate), MOE_ERR_INVALID_ARG,
+              "%s: the shared expert's two weights go together, and its gate needs them", fn);
+  MOE_REQUIRE(aligned16(x) && aligned16(y) && aligned16(norm_w) && aligned16(w_shared_gate) && aligned16(w_router) &&
+                  aligned16(w_gu) && aligned16(w_d) && aligned16(w_sh_gate_up) && aligned16(w_sh_down),
+              MOE_ERR_INVALID_ARG, "%s: operands must be 16-byte aligned", fn);
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), y0 = reinterpret_cast<uintptr_t>(y), nb = uintptr_t(T) * H * 2;
+  MOE_REQUIRE(x0 + nb <= y0 || y0 + nb <= x0, MOE_ERR_INVALID_ARG, "%s: y overlaps x", fn);
+  MOE_REQUIRE((reinterpret_cast<uintptr_t>(ws) & 255) == 0, MOE_ERR_WORKSPACE, "%s: workspace not 256-byte aligned", fn);
+  const size_t need = layer_decode_ws_bytes(T, E, k, I);
+  MOE_REQUIRE(ws_bytes >= need, MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes is too small (need %zu)", fn, ws_bytes,
+              need);
+  return layer_decode(x, T, H, norm_w, eps, w_shared_gate, w_router, bias, E, k, I, w_gu, sc_gu, w_d, sc_d, f8,
+                      w_sh_gate_up, w_sh_down, dtype, topk_idx, topk_w, y, ws, ws_bytes,
+                      static_cast<cudaStream_t>(stream));
+}
+
+int moe_layer_decode_bf16(const void* x, int T, int H, const void* norm_w, float eps, const void* w_shared_gate,
+                          const void* w_router, const float* bias, int E, int k, int I, const void* w_gate_up,
+                          const void* w_down, const void* w_sh_gate_up, const void* w_sh_down, int dtype,
+                          int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes, void* stream) {
+  return layer_decode_entry("moe_layer_decode_bf16", x, T, H, norm_w, eps, w_shared_gate, w_router, bias, E, k, I,
+                            w_gate_up, nullptr, w_down, nullptr, false, w_sh_gate_up, w_sh_down, dtype, topk_idx, topk_w,
+                            y, ws, ws_bytes, stream);
+}
+
+int moe_layer_decode_fp8_b128(const void* x, int T, int H, const void* norm_w, float eps, const void* w_shared_gate,
+                              const void* w_router, const float* bias, int E, int k, int I, const uint8_t* w_gu,
+                              const float* sc_gu, const uint8_t* w_d, const float* sc_d, const void* w_sh_gate_up,
+                              const void* w_sh_down, int dtype, int32_t* topk_idx, float* topk_w, void* y, void* ws,
+                              size_t ws_bytes, void* stream) {
+  return layer_decode_entry("moe_layer_decode_fp8_b128", x, T, H, norm_w, eps, w_shared_gate, w_router, bias, E, k, I,
+                            w_gu, sc_gu, w_d, sc_d, true, w_sh_gate_up, w_sh_down, dtype, topk_idx, topk_w, y, ws,
+                            ws_bytes, stream);
 }
 
 int moe_combine(const void* f, int f_fp32, const int32_t* slot_row, int k_slots, const float* topk_w,

@@ -15,6 +15,10 @@ forward_host(xh, yh)     pinned host x -> y in pinned host memory (copies in
                          the stream, for end-to-end measurements)
 refill_pass(x, stats)    one Refill-RMS scoring pass (k+1 slots), adds to the
                          statistics and returns y
+fused_decode=True        (the default for "fp8_b128", also for "bf16") runs
+                         forward on at most 16 tokens as one kernel
+                         (moe_layer_decode_*) where its limits allow; the
+                         "bf16" default keeps the chain of calls
 capture(x, fn)           records one pass (forward, or any callable over the
                          layer's buffers) into a CUDA graph bound to the
                          device buffer x; replaying the graph re-runs the
@@ -85,7 +89,7 @@ def prepare_fp8_weights(w: Dict[str, torch.Tensor]) -> Dict[str, torch.Tensor]:
 
 class MoELayer:
     def __init__(self, weights: Dict[str, torch.Tensor], k: int, fmt: str = "bf16", T_max: int = 8192,
-                 extra: int = 0, device: Optional[torch.device] = None):
+                 extra: int = 0, device: Optional[torch.device] = None, fused_decode: Optional[bool] = None):
         self.w = weights
         self.k = k
         self.fmt = fmt
@@ -117,6 +121,9 @@ class MoELayer:
             self.I = weights["w8_gu"].shape[1] // 2
         else:
             raise ValueError(fmt)
+        if fused_decode and fmt not in ("bf16", "fp8_b128"):
+            raise ValueError(f"fused_decode: no one-kernel layer for {fmt}")
+        self.fused_decode = fmt == "fp8_b128" if fused_decode is None else fused_decode
         self._alloc(T_max)
 
     def _alloc(self, T_max: int) -> None:
@@ -160,6 +167,13 @@ class MoELayer:
             self.ws_exp = torch.empty(max(256, need), dtype=torch.uint8, device=d)
         else:
             self.ws_exp = None
+        # one-kernel decode: bytes for each T it takes (0: outside its limits)
+        self.decode_ws = {}
+        if self.fused_decode and not self.extra and self.I_sh == self.I:
+            need = {t: abi.moe_workspace_size(abi.MOE_OP_LAYER_DECODE, t, H, E, self.k, self.I)
+                    for t in range(1, min(T_max, 16) + 1)}
+            self.decode_ws = {t: n for t, n in need.items() if n}
+            self.ws_decode = torch.empty(max(self.decode_ws.values(), default=256), dtype=torch.uint8, device=d)
         self.ws_refill = abi.workspace(abi.MOE_OP_REFILL, T_max, H, E, ks, 0, d)
         self._sh_off = {}
 
@@ -258,12 +272,26 @@ class MoELayer:
         into the layer's own output buffer (overwritten by the next pass)."""
         T = x.shape[0]
         assert T <= self.T_max and self.extra == 0
+        if T in self.decode_ws:
+            return self._forward_decode(x, self.y[:T] if y is None else y)
         xin = self.route(x)
         gate = self.block_gate(xin)
         f, sh = self.experts_and_shared(xin)
         y = self.y[:T] if y is None else y
         abi.moe_combine(f, self.slot_row[:T], self.topk_w[:T], shared_out=sh, shared_gate=gate, y=y)
         return y
+
+    def _forward_decode(self, x: torch.Tensor, y: torch.Tensor) -> torch.Tensor:
+        """forward of a few tokens as one kernel; the selection is left in
+        topk_idx and topk_w."""
+        T, w = x.shape[0], self.w
+        rest = dict(w_sh_gate_up=w["w_sh_gate_up"], w_sh_down=w["w_sh_down"], norm_w=w.get("w_norm"),
+                    eps=self.norm_eps, w_shared_gate=w.get("w_sh_gate"), topk_idx=self.topk_idx[:T],
+                    topk_w=self.topk_w[:T], y=y, ws=self.ws_decode)
+        if self.fmt == "fp8_b128":
+            return abi.moe_layer_decode_fp8_b128(x, w["w_router"], w["bias"], self.k, w["w8_gu"], w["sc8_gu"],
+                                                 w["w8_d"], w["sc8_d"], **rest)
+        return abi.moe_layer_decode_bf16(x, w["w_router"], w["bias"], self.k, w["w_gate_up"], w["w_down"], **rest)
 
     def shared_gate(self, x: torch.Tensor) -> Optional[torch.Tensor]:
         """Per-token shared-expert gate (moe_shared_gate), or None without one."""

@@ -517,6 +517,44 @@ MOE_API int moe_grouped_swiglu_fp8_b128(const void* x, const int32_t* row_token,
                                         void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * A whole MoE layer on a few tokens in one kernel [ARCH]: optional pre-MoE
+ * RMSNorm (x_norm = x / sqrt(mean x^2 + eps) * (1 + norm_w), rounded to dtype),
+ * router logits (+ bias), top-k with renormalised weights (ties to the lower
+ * expert index), the selected SwiGLU experts, the optional shared expert with
+ * its optional gate sigmoid(x_norm . w_shared_gate), and
+ *   y[t] = sum_j topk_w[t, j] * f_j(x_norm[t]) (+ gate[t] * shared(x_norm[t]))
+ * summed in FP32 and rounded once to dtype.  _bf16: experts of `dtype` (as
+ * moe_experts_bf16; h is rounded to dtype).  _fp8_b128: FP8 experts (as
+ * moe_grouped_swiglu_fp8_b128: x_norm and h quantised per 128 features); the
+ * router and the shared expert stay of `dtype`.
+ * The router's logits are summed in FP64, so a near-tie resolves by the exact
+ * logits rounded to FP32; NaN logits rank last; a token needs at least one
+ * finite logit for its weights to be numbers.
+ * x, y [T, H] dtype (y must not overlap x); norm_w [H] or NULL; w_shared_gate
+ * [H] or NULL (needs the shared expert); w_router [E, H]; bias [E] FP32 or
+ * NULL; expert weights and scales as in the calls named above; w_sh_gate_up
+ * [2I, H] and w_sh_down [H, I], or both NULL; topk_idx [T, k] int32 and topk_w
+ * [T, k] FP32, or NULL.
+ * One cooperative launch over all SMs: calls on different streams run one
+ * after the other.  Limits: T <= 16, H % 64 == 0, H <= 4096, T * H <= 40960,
+ * I % 64 == 0, I <= 8192, 1 <= k <= 16, k <= E <= 1024; x, y and all weights
+ * 16-byte aligned.
+ * Workspace: MOE_OP_LAYER_DECODE (k_slots = k), not shared with a call that
+ * may run at the same time.
+ * ------------------------------------------------------------------------- */
+MOE_API int moe_layer_decode_bf16(const void* x, int T, int H, const void* norm_w, float eps,
+                                  const void* w_shared_gate, const void* w_router, const float* bias, int E, int k,
+                                  int I, const void* w_gate_up, const void* w_down, const void* w_sh_gate_up,
+                                  const void* w_sh_down, int dtype, int32_t* topk_idx, float* topk_w, void* y, void* ws,
+                                  size_t ws_bytes, void* stream);
+MOE_API int moe_layer_decode_fp8_b128(const void* x, int T, int H, const void* norm_w, float eps,
+                                      const void* w_shared_gate, const void* w_router, const float* bias, int E, int k,
+                                      int I, const uint8_t* w_gu, const float* sc_gu, const uint8_t* w_d,
+                                      const float* sc_d, const void* w_sh_gate_up, const void* w_sh_down, int dtype,
+                                      int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes,
+                                      void* stream);
+
+/* ---------------------------------------------------------------------------
  * Weighted combine [ARCH]:
  *   y[t] = sum_{j<k} topk_w[t, j] * f[slot_row[t, j]]  (+ gate[t] * shared[t])
  * summed in FP32 in slot order, rounded once to dtype.
