@@ -22,14 +22,18 @@
 // With row_token, A rows are gathered by four warps with cp.async straight
 // into the 128-byte-swizzled A tile; rows past the group read zero.
 //
-// Warp roles: 0 TMA producer, 1 UMMA issuer (TMEM owner), 2 and 3 idle (they
-// complete a register-allocation group), 4..7 A-row gather, 8..15 promotion
+// Warp roles: 0 TMA producer, 1 and 2 UMMA issuers of the even and the odd K
+// steps (one thread's waits, issue and commits take about 800 cycles a step, the
+// products 545; 1 owns the TMEM), 3 scales (row scale x column block scale of every
+// step into shared memory, ahead of the promotion warps), 4..7 A-row gather, 8..15 promotion
 // and epilogue (two per 32 rows, each half of the tile's columns).
 #include "fp8.cuh"
 #include "gemm_sm100.cuh"
 
 namespace moe {
 
+int make_tmap_2d(CUtensorMap* map, const void* base, int rows, int cols, int esize, int box_rows, int box_cols,
+                 CUtensorMapSwizzle swz);
 int make_tmap_2d_u8_sw128(CUtensorMap* map, const void* base, int rows, int cols_bytes, int box_rows);
 int fp8_quantize(const void* v, int batch, int rows, int K, int block_rows, int dtype, uint8_t* codes, float* scales,
                  cudaStream_t stream);
@@ -42,18 +46,22 @@ constexpr int A_BYTES = BM * BK;
 constexpr int kThreads = 512;
 constexpr int kGatherWarp0 = 4;
 constexpr int kEpiWarp0 = 8;
-constexpr int kSmemBudget = 200 * 1024;
+constexpr int kSmemBudget = 212 * 1024;
+constexpr int kStoreStride = 64 + 16;  // output staging: bytes per row of a 64-byte chunk, padded
+constexpr int kBoxBytes = 32 * 128;    // 16-bit output: a box of 32 rows x 64 columns, two per warp
 // registers per thread of the role groups: the sum over the four groups of
 // 128 threads is what the block is launched with (512 x 128)
-constexpr int kRegsIssue = 64, kRegsGather = 64, kRegsEpi = 192;
+constexpr int kRegsIssue = 48, kRegsGather = 48, kRegsEpi = 208;
 static_assert(kRegsIssue + kRegsGather + 2 * kRegsEpi == 4 * 128, "register split must equal the launch's total");
 
-template <int BN>
+template <int BN, bool SWIGLU>
 struct Cfg {
   static constexpr int B_BYTES = BN * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = kSmemBudget / STAGE_BYTES > 8 ? 8 : kSmemBudget / STAGE_BYTES;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+  static constexpr int STORE_BYTES = SWIGLU ? 8 * 32 * kStoreStride : 8 * 2 * kBoxBytes;
+  static constexpr int STAGES = (kSmemBudget - STORE_BYTES) / STAGE_BYTES;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + STORE_BYTES;
+  static_assert(32 * kStoreStride <= 2 * kBoxBytes, "a warp's staging area serves both store forms");
   static constexpr int NACC = 512 / BN;  // TMEM accumulator ring
   static_assert(STAGE_BYTES % 1024 == 0, "stage must keep 1024-byte alignment");
 };
@@ -92,6 +100,65 @@ __device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src,
 __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// A TMEM load of 32 columns and its wait as two steps, so that the arithmetic on
+// one chunk runs while the next is on its way.  The wait names the registers,
+// which keeps their use behind it.
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t ta, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%"
+      "19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(ta)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+// Two FP32 numbers in one register pair.
+__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(a), "r"(b));
+  return v;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+
+// Stores a chunk of 64 bytes per row (one row per lane) through the warp's
+// staging area: four lanes write one row's 64 bytes, eight rows an instruction,
+// instead of 16 bytes of 32 rows.  Rows from nvalid on and bytes from nbytes on
+// are left alone.
+__device__ __forceinline__ void warp_store_64(uint8_t* stg, const uint32_t (&v)[16], int nvalid, int nbytes, uint8_t* gbase,
+                                              size_t pitch, int lane) {
+  uint4* mine = reinterpret_cast<uint4*>(stg + lane * kStoreStride);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mine[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  __syncwarp();
+  const int seg = lane & 3;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const int r = p * 8 + (lane >> 2);
+    const uint4 w = *reinterpret_cast<const uint4*>(stg + r * kStoreStride + seg * 16);
+    if (r < nvalid && seg * 16 < nbytes) st_global_v4(gbase + size_t(r) * pitch + seg * 16, w.x, w.y, w.z, w.w);
+  }
+  __syncwarp();
+}
+
 template <int R>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
@@ -99,6 +166,34 @@ __device__ __forceinline__ void regs_inc() {
 template <int R>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// mbar_wait for the waits on the path from one K step to the next: polls
+// instead of suspending.  Bounded the same way.
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                          unsigned long long limit_ns) {
+  unsigned long long t0 = 0;
+  for (uint32_t spins = 0;; ++spins) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((spins & 1023u) == 1023u) {
+      const unsigned long long now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (*abort_flag) return false;
+      if (now - t0 > limit_ns) {
+        report(status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
 }
 
 struct TileMap {
@@ -155,20 +250,21 @@ __device__ __forceinline__ TileMap decode_tile(int L, int nt, const int* tile_st
 template <int BN, bool SWIGLU>
 __global__ void __launch_bounds__(kThreads, 1)
     k_grouped_gemm_fp8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                       const Args args) {
-  using C = Cfg<BN>;
+                       const __grid_constant__ CUtensorMap tmO, const Args args) {
+  using C = Cfg<BN, SWIGLU>;
   constexpr int STAGES = C::STAGES, NACC = C::NACC;
   constexpr int BNH = SWIGLU ? BN / 2 : BN;  // output columns per tile
   constexpr int NC = BN / 2;                 // accumulator columns per promotion thread
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES], tfull_bar[NACC], tempty_bar[NACC], xbar[4],
-      drain_bar;
+      drain_bar[2];
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_flag;
   __shared__ int goff[kGemmMaxGroups + 1];
   __shared__ int tile_start[kGemmMaxGroups + 1];
   __shared__ int warp_sums[kThreads / 32];
   __shared__ float row_max[2][2][BM];
+  __shared__ float step_scale[NACC][2][BM];  // of each accumulator: row scale x the two column blocks' scales
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   auto stg = [&](int s) { return smem + s * C::STAGE_BYTES; };
@@ -180,11 +276,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&empty_bar[s], 1);
     }
     for (int i = 0; i < NACC; ++i) {
-      mbar_init(&tfull_bar[i], 1);
+      mbar_init(&tfull_bar[i], 2);   // the products' commit and the scale warp
       mbar_init(&tempty_bar[i], 8);  // one arrival per promotion warp
     }
     for (int i = 0; i < 4; ++i) mbar_init(&xbar[i], 2);  // the two warps of a row quadrant
-    mbar_init(&drain_bar, 1);
+    mbar_init(&drain_bar[0], 1);
+    mbar_init(&drain_bar[1], 1);
     abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
@@ -235,36 +332,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (long i = (issued > STAGES ? issued - STAGES : 0); i < issued; ++i)
           mbar_wait(&full_bar[i % STAGES], uint32_t((i / STAGES) & 1), &never, nullptr, lim);
       }
-    } else if (warp == 1 && lane == 0) {
-      // ---------------- UMMA issuer ----------------
+    } else if ((warp == 1 || warp == 2) && lane == 0) {
+      // ---------------- UMMA issuers ----------------
+      // Steps are counted over all tiles; this thread issues those of its parity.
       constexpr uint32_t idesc = idesc_e4m3(BN);
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, buf_phase = 0;
+      const long tiles = total > int(blockIdx.x) ? (total - int(blockIdx.x) + gridDim.x - 1) / gridDim.x : 0;
+      const long steps = tiles * KB;
+      for (long i = warp - 1; i < steps; i += 2) {
+        const int stage = int(i % STAGES), buf = int(i % NACC);
+        const uint32_t phase = uint32_t(i / STAGES) & 1, buf_phase = uint32_t(i / NACC) & 1;
+        if (!mbar_poll(&tempty_bar[buf], buf_phase ^ 1, &abort_flag, status, lim) ||
+            !mbar_poll(&full_bar[stage], phase, &abort_flag, status, lim))
+          break;
+        if (gathered) fence_proxy_async_smem();  // the gathered rows were written through the generic proxy
+        tc_fence_after();
+        const uint32_t sbase = smem_u32(stg(stage));
+        const uint64_t ad = sdesc_kmajor_sw128(sbase), bd = sdesc_kmajor_sw128(sbase + A_BYTES);
+        const uint32_t d = tmem_base + uint32_t(buf * BN);
+#pragma unroll
+        for (int j = 0; j < BK / 32; ++j)  // K = 32 per MMA: 32 bytes along the swizzled row
+          umma_f8(d, ad + uint64_t(2 * j), bd + uint64_t(2 * j), idesc, j != 0);
+        umma_commit(&tfull_bar[buf]);
+        umma_commit(&empty_bar[stage]);
+      }
+      umma_commit(&drain_bar[warp - 1]);
+      volatile int never = 0;
+      mbar_wait(&drain_bar[warp - 1], 0, &never, nullptr, lim);
+    }
+    if (warp == 3) {
+      // ---------------- scales ----------------
+      int buf = 0;
+      uint32_t buf_phase = 0;
       bool ok = true;
       for (int L = blockIdx.x; L < total && ok; L += gridDim.x) {
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait(&tempty_bar[buf], buf_phase ^ 1, &abort_flag, status, lim) ||
-              !mbar_wait(&full_bar[stage], phase, &abort_flag, status, lim)) {
-            ok = false;
-            break;
-          }
-          if (gathered) fence_proxy_async_smem();  // the gathered rows were written through the generic proxy
-          tc_fence_after();
-          const uint32_t sbase = smem_u32(stg(stage));
-          const uint64_t ad = sdesc_kmajor_sw128(sbase), bd = sdesc_kmajor_sw128(sbase + A_BYTES);
-          const uint32_t d = tmem_base + uint32_t(buf * BN);
+        const TileMap t = decode_tile(L, nt, tile_start, G);
+        const int row0 = goff[t.g] + t.m * BM;
+        const int tile_rows = min(BM, min(goff[t.g + 1], args.rows) - row0);
+        int src[4];  // scale rows of tile rows lane, lane + 32, ..; -1: no row
 #pragma unroll
-          for (int j = 0; j < BK / 32; ++j)  // K = 32 per MMA: 32 bytes along the swizzled row
-            umma_f8(d, ad + uint64_t(2 * j), bd + uint64_t(2 * j), idesc, j != 0);
-          umma_commit(&empty_bar[stage]);
-          umma_commit(&tfull_bar[buf]);
-          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        for (int i = 0; i < 4; ++i) {
+          const int r = lane + 32 * i;
+          int v = r < tile_rows ? row0 + r : -1;
+          if (gathered && v >= 0) v = __ldg(args.row_token + v);
+          src[i] = v >= 0 && v < args.a_rows ? v : -1;
+        }
+        // the two column blocks: gate and up, or the tile's halves
+        const int nb0 = t.n * BNH / kFp8Block, nb1 = SWIGLU ? nb0 : min(nb0 + BN / 2 / kFp8Block, args.w_blocks - 1);
+        const float* sw0 = args.sw + (size_t(t.g) * (SWIGLU ? 2 : 1) * args.w_blocks + nb0) * KB;
+        const float* sw1 = args.sw + ((size_t(t.g) * (SWIGLU ? 2 : 1) + (SWIGLU ? 1 : 0)) * args.w_blocks + nb1) * KB;
+        float a[4], w0 = __ldg(sw0), w1 = __ldg(sw1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = src[i] >= 0 ? __ldg(args.sa + size_t(src[i]) * KB) : 0.0f;
+        for (int kb = 0; kb < KB; ++kb) {
+          float na[4] = {0.0f, 0.0f, 0.0f, 0.0f}, nw0 = 0.0f, nw1 = 0.0f;
+          if (kb + 1 < KB) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) na[i] = src[i] >= 0 ? __ldg(args.sa + size_t(src[i]) * KB + kb + 1) : 0.0f;
+            nw0 = __ldg(sw0 + kb + 1);
+            nw1 = __ldg(sw1 + kb + 1);
+          }
+          if (!mbar_poll(&tempty_bar[buf], buf_phase ^ 1, &abort_flag, status, lim)) { ok = false; break; }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            step_scale[buf][0][lane + 32 * i] = a[i] * w0;
+            step_scale[buf][1][lane + 32 * i] = a[i] * w1;
+            a[i] = na[i];
+          }
+          w0 = nw0;
+          w1 = nw1;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tfull_bar[buf]);
           if (++buf == NACC) { buf = 0; buf_phase ^= 1; }
         }
       }
-      umma_commit(&drain_bar);
-      volatile int never = 0;
-      mbar_wait(&drain_bar, 0, &never, nullptr, lim);
     }
   } else if (warp < kEpiWarp0) {
     regs_dec<kRegsGather>();
@@ -321,64 +461,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       // columns of this thread: output columns col0 .. (SwiGLU: BNH/2 of them, gate and up)
       const int col0 = t.n * BNH + half * (SWIGLU ? BNH / 2 : NC);
       const bool live = q * 32 < tile_rows && col0 < args.n_out;  // uniform in the warp
-      const float* sa = args.sa;
-      bool row_ok = valid;
-      if (valid) {
-        int src = int(out_row);
-        if (gathered) src = __ldg(args.row_token + out_row);
-        row_ok = src >= 0 && src < args.a_rows;
-        sa += size_t(row_ok ? src : 0) * KB;
-      }
       const int nb = col0 / kFp8Block;
-      const float* sw0 = args.sw + (SWIGLU ? (size_t(t.g) * 2 * args.w_blocks + nb) : (size_t(t.g) * args.w_blocks + nb)) * KB;
-      const float* sw1 = sw0 + (SWIGLU ? size_t(args.w_blocks) * KB : 0);
-      float acc[NC];
+      uint64_t acc[NC / 2];  // pairs of neighbouring columns
 #pragma unroll
-      for (int i = 0; i < NC; ++i) acc[i] = 0.0f;
-      float na = 0.0f, n0 = 0.0f, n1 = 0.0f;
-      if (live) {
-        na = row_ok ? __ldg(sa) : 0.0f;
-        n0 = __ldg(sw0);
-        n1 = SWIGLU ? __ldg(sw1) : n0;
-      }
+      for (int i = 0; i < NC / 2; ++i) acc[i] = 0;
       const uint32_t lane_base = tmem_base + (uint32_t(q * 32) << 16);
       for (int kb = 0; kb < KB; ++kb) {
-        const float s0 = na * n0, s1 = na * n1;
-        if (live && kb + 1 < KB) {
-          na = row_ok ? __ldg(sa + kb + 1) : 0.0f;
-          n0 = __ldg(sw0 + kb + 1);
-          n1 = SWIGLU ? __ldg(sw1 + kb + 1) : n0;
-        }
-        if (!mbar_wait(&tfull_bar[buf], buf_phase, &abort_flag, status, lim)) { ok = false; break; }
+        if (!mbar_poll(&tfull_bar[buf], buf_phase, &abort_flag, status, lim)) { ok = false; break; }
         tc_fence_after();
         if (live) {
+          const uint32_t s0 = __float_as_uint(step_scale[buf][SWIGLU ? 0 : half][row_in_tile]);
+          const uint32_t s1 = SWIGLU ? __float_as_uint(step_scale[buf][1][row_in_tile]) : s0;
+          const uint64_t p0 = pack2(s0, s0), p1 = pack2(s1, s1);
+          // SwiGLU: the first half of the chunks are gate columns, the rest the matching up columns
+          constexpr int CH = NC / 32;
+          auto col_of = [&](int c) {
+            return SWIGLU ? (c < CH / 2 ? half * (BNH / 2) + 32 * c : BNH + half * (BNH / 2) + 32 * (c - CH / 2))
+                          : half * NC + 32 * c;
+          };
+          const uint32_t tb = lane_base + uint32_t(buf * BN);
+          // two chunks on their way at a time: the next two are requested as the registers come free
+          uint32_t v[2][32];
+          tmem_ld32_issue(tb + col_of(0), v[0]);
+          tmem_ld32_issue(tb + col_of(1), v[1]);
 #pragma unroll
-          for (int c = 0; c < NC / 32; ++c) {
-            // SwiGLU: the first half of the chunks are gate columns, the rest the matching up columns
-            const int col = SWIGLU ? (c < NC / 64 ? half * (BNH / 2) + 32 * c : BNH + half * (BNH / 2) + 32 * (c - NC / 64))
-                                   : half * NC + 32 * c;
-            const float s = SWIGLU && c >= NC / 64 ? s1 : s0;
-            float v[32];
-            tmem_ld32(lane_base + uint32_t(buf * BN + col), v);
+          for (int c = 0; c < CH; ++c) {
+            if ((c & 1) == 0) {
+              tmem_ld32_wait(v[0]);
+              tmem_ld32_wait(v[1]);
+              if (c + 2 == CH) {  // all columns are in registers: the buffer is free
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+              }
+            }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(v[i], s, acc[32 * c + i]);
+            for (int i = 0; i < 16; ++i)
+              fma2(acc[16 * c + i], pack2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), SWIGLU && c >= CH / 2 ? p1 : p0);
+            if (c + 2 < CH) tmem_ld32_issue(tb + col_of(c + 2), v[c & 1]);
           }
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty_bar[buf]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty_bar[buf]);
         if (++buf == NACC) { buf = 0; buf_phase ^= 1; }
       }
       if (!ok) break;
+      uint8_t* stg_w = smem + STAGES * C::STAGE_BYTES + (warp - kEpiWarp0) * (SWIGLU ? 32 * kStoreStride : 2 * kBoxBytes);
+      const int nvalid = tile_rows - q * 32;  // rows of this warp that exist
+      const size_t row0 = size_t(goff[t.g]) + size_t(t.m) * BM + q * 32;
       if (SWIGLU) {
         constexpr int NH = NC / 2;  // h columns of this thread
+        float h[NH];
         float amax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NH; ++i) {
-          const float g = acc[i];
-          acc[i] = (g / (1.0f + __expf(-g))) * acc[NH + i];
-          if (col0 + (i & ~31) >= args.n_out) acc[i] = 0.0f;  // n_out is a multiple of 64: whole chunks
-          amax = fmaxf(amax, fabsf(acc[i]));
+        for (int i = 0; i < NH / 2; ++i) {
+          const float2 g = unpack2(acc[i]), u = unpack2(acc[NH / 2 + i]);
+          h[2 * i] = __fdividef(g.x, 1.0f + __expf(-g.x)) * u.x;
+          h[2 * i + 1] = __fdividef(g.y, 1.0f + __expf(-g.y)) * u.y;
+          if (col0 + ((2 * i) & ~31) >= args.n_out) h[2 * i] = h[2 * i + 1] = 0.0f;  // n_out is a multiple of 64
+          amax = fmaxf(amax, fmaxf(fabsf(h[2 * i]), fabsf(h[2 * i + 1])));
         }
         if (!live) amax = 0.0f;
         row_max[x_phase][half][row_in_tile] = amax;
@@ -387,47 +530,81 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(&xbar[q], x_phase, &abort_flag, status, lim)) break;
         amax = fmaxf(amax, row_max[x_phase][half ^ 1][row_in_tile]);
         x_phase ^= 1;
-        if (live && valid) {
+        if (live) {
           const Fp8Scale s = fp8_scale(amax);
-          uint8_t* dst = static_cast<uint8_t*>(args.out) + out_row * args.n_out + col0;
+          uint32_t p[16];
 #pragma unroll
-          for (int i = 0; i < NH / 16; ++i) {
-            uint32_t p[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float* a = acc + 16 * i + 4 * j;
-              p[j] = fp8_quant4(a[0], a[1], a[2], a[3], s.r);
-            }
-            st_global_v4(dst + 16 * i, p[0], p[1], p[2], p[3]);
-          }
-          if (half == 0) args.out_scales[out_row * args.w_blocks + nb] = s.s;
+          for (int i = 0; i < 16; ++i) p[i] = fp8_quant4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3], s.r);
+          warp_store_64(stg_w, p, nvalid, 64, static_cast<uint8_t*>(args.out) + row0 * args.n_out + col0, args.n_out, lane);
+          if (half == 0 && valid) args.out_scales[out_row * args.w_blocks + nb] = s.s;
         }
-      } else if (live && valid) {
-        const size_t at = out_row * args.n_out + col0;
+      } else if (live) {
+        if (args.out_kind == 2) {
 #pragma unroll
-        for (int i = 0; i < NC / 8; ++i) {
-          if (col0 + 8 * i >= args.n_out) break;
-          const float* a = acc + 8 * i;
-          if (args.out_kind == 2) {
-            float* dst = static_cast<float*>(args.out) + at + 8 * i;
-            st_global_v4(dst, __float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]),
-                         __float_as_uint(a[3]));
-            st_global_v4(dst + 4, __float_as_uint(a[4]), __float_as_uint(a[5]), __float_as_uint(a[6]),
-                         __float_as_uint(a[7]));
-          } else {
-            uint16_t* dst = static_cast<uint16_t*>(args.out) + at + 8 * i;
-            uint32_t p[4];
+          for (int c = 0; c < NC / 16; ++c) {
+            if (col0 + 16 * c >= args.n_out) break;
+            uint32_t p[16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              p[j] = args.out_kind == 0 ? Pack2<__nv_bfloat16>::pack(a[2 * j], a[2 * j + 1])
-                                        : Pack2<__half>::pack(a[2 * j], a[2 * j + 1]);
-            st_global_v4(dst, p[0], p[1], p[2], p[3]);
+            for (int i = 0; i < 8; ++i) {
+              const float2 f = unpack2(acc[8 * c + i]);
+              p[2 * i] = __float_as_uint(f.x);
+              p[2 * i + 1] = __float_as_uint(f.y);
+            }
+            warp_store_64(stg_w, p, nvalid, 64, static_cast<uint8_t*>(args.out) + (row0 * args.n_out + col0 + 16 * c) * 4,
+                          size_t(args.n_out) * 4, lane);
           }
+        } else {
+          // boxes of 32 rows x 64 columns: written to shared memory in the 128-byte
+          // swizzle and copied out by the tensor copy unit (whole lines, and the warp
+          // goes on), or by the warp where rows are missing (they belong to the next
+          // group)
+          auto store16 = [&](auto pack) {
+#pragma unroll
+            for (int c = 0; c < NC / 64; ++c) {
+              if (col0 + 64 * c >= args.n_out) break;
+              uint8_t* box = stg_w + (c & 1) * kBoxBytes;
+              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the copy before last has read
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                uint32_t p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[i] = pack(unpack2(acc[32 * c + 4 * k + i]));
+                *reinterpret_cast<uint4*>(box + lane * 128 + ((k ^ (lane & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+              }
+              if (nvalid >= 32) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                                   reinterpret_cast<uint64_t>(&tmO)),
+                               "r"(smem_u32(box)), "r"(col0 + 64 * c), "r"(int(row0))
+                               : "memory");
+              } else {
+                __syncwarp();
+                const int seg = lane & 7;
+                uint8_t* dst = static_cast<uint8_t*>(args.out) + (row0 * args.n_out + col0 + 64 * c) * 2 + seg * 16;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const int r = k * 4 + (lane >> 3);
+                  const uint4 w = *reinterpret_cast<const uint4*>(box + r * 128 + ((seg ^ (r & 7)) << 4));
+                  if (r < nvalid && col0 + 64 * c + seg * 8 < args.n_out)
+                    st_global_v4(dst + size_t(r) * args.n_out * 2, w.x, w.y, w.z, w.w);
+                }
+              }
+              if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+          };
+          if (args.out_kind == 0)
+            store16([](float2 f) { return Pack2<__nv_bfloat16>::pack(f.x, f.y); });
+          else
+            store16([](float2 f) { return Pack2<__half>::pack(f.x, f.y); });
         }
       }
     }
   }
 
+  if (!SWIGLU && warp >= kEpiWarp0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -443,15 +620,20 @@ int launch(const Args& a, const uint8_t* w, int w_rows, cudaStream_t stream) {
   if (rc) return rc;
   rc = make_tmap_2d_u8_sw128(&tb, w, w_rows, a.K, SWIGLU ? BN / 2 : BN);
   if (rc) return rc;
+  CUtensorMap to = ta;  // only 16-bit outputs are stored through a map
+  if (!SWIGLU && a.out_kind != 2) {
+    rc = make_tmap_2d(&to, a.out, a.rows, a.n_out, 2, 32, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc) return rc;
+  }
   auto kern = k_grouped_gemm_fp8<BN, SWIGLU>;
   static bool attr_set[64] = {false};
   int dev = 0;
   MOE_CHECK_CUDA(cudaGetDevice(&dev));
   if (dev >= 64 || !attr_set[dev]) {
-    MOE_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::SMEM_BYTES));
+    MOE_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN, SWIGLU>::SMEM_BYTES));
     if (dev < 64) attr_set[dev] = true;
   }
-  kern<<<num_sms(), kThreads, Cfg<BN>::SMEM_BYTES, stream>>>(ta, tb, a);
+  kern<<<num_sms(), kThreads, Cfg<BN, SWIGLU>::SMEM_BYTES, stream>>>(ta, tb, to, a);
   MOE_CHECK_CUDA(cudaGetLastError());
   return MOE_OK;
 }
