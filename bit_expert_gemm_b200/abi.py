@@ -125,12 +125,13 @@ def _p(t: Optional[torch.Tensor]):
         raise ValueError("expected a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -527,10 +528,11 @@ def moe_grouped_swiglu_nvfp4_prepacked(x, row_token, expert_offsets, rows: int, 
 def _same_device(x: torch.Tensor, *others: Optional[torch.Tensor]):
     """All operands on x's device, and that device current: the library
     launches on the current device."""
+    d = x.get_device()
     for t in others:
-        if t is not None and t.device != x.device:
+        if t is not None and t.get_device() != d:
             raise ValueError(f"operands on {x.device} and {t.device}")
-    if x.is_cuda and x.device.index != torch.cuda.current_device():
+    if d >= 0 and d != torch._C._cuda_getDevice():
         raise ValueError(f"operands are on {x.device}, but the current device is cuda:{torch.cuda.current_device()}")
 
 
@@ -541,7 +543,7 @@ def _fp8_codes(t: torch.Tensor, name: str):
 
 def _fp8_shape(t: torch.Tensor, shape, name: str):
     _need(t, torch.float32, name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -558,10 +560,10 @@ def moe_fp8_quantize_b128(v, block_rows: int = 1, codes=None, scales=None, strea
         raise ValueError("moe_fp8_quantize_b128: v must be [rows, K] or [batch, rows, K]")
     R, K = v.shape[-2:]
     if codes is None:
-        codes = torch.empty(v.shape, dtype=torch.float8_e4m3fn, device=v.device)
+        codes = torch.empty_like(v, dtype=torch.float8_e4m3fn)
     sshape = (*v.shape[:-2], (R + block_rows - 1) // max(1, block_rows), _blocks(K))
     if scales is None:
-        scales = torch.empty(sshape, dtype=torch.float32, device=v.device)
+        scales = v.new_empty(sshape, dtype=torch.float32)
     _fp8_codes(codes, "codes")
     _fp8_shape(scales, sshape, "scales")
     if codes.shape != v.shape:
@@ -596,7 +598,7 @@ def moe_grouped_gemm_fp8_b128(a, a_scales, w, w_scales, expert_offsets=None, row
             raise ValueError(f"expert_offsets: expected {E + 1} entries, got {expert_offsets.numel()}")
     if out is None:
         out = torch.empty((rows, N), dtype=out_dtype, device=a.device)
-    if tuple(out.shape) != (rows, N):
+    if out.shape != (rows, N):
         raise ValueError(f"out: expected shape {(rows, N)}, got {tuple(out.shape)}")
     _same_device(a, a_scales, w, w_scales, expert_offsets, row_token, out)
     fp32 = out.dtype == torch.float32
@@ -608,7 +610,7 @@ def moe_grouped_gemm_fp8_b128(a, a_scales, w, w_scales, expert_offsets=None, row
 def _fp8_experts(H: int, E: int, I: int, w_gu, sc_gu, w_d, sc_d):
     _fp8_codes(w_gu, "w_gu")
     _fp8_codes(w_d, "w_d")
-    if tuple(w_gu.shape) != (E, 2 * I, H) or tuple(w_d.shape) != (E, H, I):
+    if w_gu.shape != (E, 2 * I, H) or w_d.shape != (E, H, I):
         raise ValueError(f"FP8 experts: w_gu must be [E, 2I, H] and w_d [E, H, I], got {tuple(w_gu.shape)} and "
                          f"{tuple(w_d.shape)} for H={H}")
     _fp8_shape(sc_gu, (E, 2, _blocks(I), _blocks(H)), "sc_gu")
@@ -633,7 +635,7 @@ def moe_grouped_swiglu_fp8_b128(x, row_token, expert_offsets, rows: int, w_gu, s
             raise ValueError(f"row_token: {row_token.numel()} entries for {rows} rows")
     if f is None:
         f = torch.empty((rows, H), dtype=torch.float32 if out_fp32 else x.dtype, device=dev)
-    if tuple(f.shape) != (rows, H) or f.dtype != (torch.float32 if out_fp32 else x.dtype):
+    if f.shape != (rows, H) or f.dtype != (torch.float32 if out_fp32 else x.dtype):
         raise ValueError(f"f: expected [{rows}, {H}] of {'float32' if out_fp32 else x.dtype}")
     if ws is None:
         ws = workspace(MOE_OP_SWIGLU_FP8_B128, T, H, E, max(1, -(-rows // max(T, 1))), I, dev)
@@ -649,7 +651,7 @@ def _layer_decode(name, x, w_router, bias, k, I, experts, w_sh_gate_up, w_sh_dow
     E = w_router.shape[0]
 
     def need(t, shape, what, dtype=x.dtype):
-        if t is not None and (t.dtype != dtype or tuple(t.shape) != shape):
+        if t is not None and (t.dtype != dtype or t.shape != shape):
             raise ValueError(f"{name}: {what} must be {list(shape)} of {dtype}, got {list(t.shape)} of {t.dtype}")
 
     need(w_router, (E, H), "w_router")
@@ -680,7 +682,7 @@ def moe_layer_decode_bf16(x, w_router, bias, k: int, w_gate_up, w_down, w_sh_gat
     its gate, weighted sum.  Returns y [T, H]; topk_idx [T, k] int32 and
     topk_w [T, k] FP32 receive the selection when given."""
     E, I2, H = w_gate_up.shape
-    if w_gate_up.dtype != x.dtype or w_down.dtype != x.dtype or tuple(w_down.shape) != (E, H, I2 // 2) or \
+    if w_gate_up.dtype != x.dtype or w_down.dtype != x.dtype or w_down.shape != (E, H, I2 // 2) or \
             (E, H) != (w_router.shape[0], x.shape[1]):
         raise ValueError(f"moe_layer_decode_bf16: experts [E, 2I, H] and [E, H, I] of {x.dtype} expected, got "
                          f"{list(w_gate_up.shape)} and {list(w_down.shape)}")

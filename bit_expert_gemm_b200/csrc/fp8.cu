@@ -32,31 +32,56 @@ __device__ __forceinline__ uint2 quant8(const float (&v)[8], float r) {
   return make_uint2(fp8_quant4(v[0], v[1], v[2], v[3], r), fp8_quant4(v[4], v[5], v[6], v[7], r));
 }
 
-// 1 x 128 blocks: 16 lanes of 8 values each hold one block.  `rows` counts
-// the rows of all batches (they are contiguous).
+// 1 x 128 blocks: 16 lanes of 8 values each hold one block, four blocks at a
+// time (64 bytes a lane in flight).  The two divisions of a block cost as much
+// as all its other arithmetic when every lane does them, so lane i of the four
+// blocks' 16 does those of block i and the others are told.  `rows` counts the
+// rows of all batches (they are contiguous).
+constexpr int kBlocks = 4;
 template <typename T16>
 __global__ void __launch_bounds__(kThreads) k_fp8_quant_rows(const T16* __restrict__ v, size_t rows, int K,
                                                              uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  griddep_wait();
+  griddep_launch_dependents();
   const int KB = fp8_blocks(K);
   const size_t total = rows * size_t(KB);
-  const int sub = threadIdx.x & 15;
-  const size_t stride = size_t(gridDim.x) * (kThreads / 16);
+  const int lane = threadIdx.x & 31, sub = lane & 15;
+  const size_t per_cta = kThreads / 16 * kBlocks, stride = size_t(gridDim.x) * per_cta;
   // both halves of a warp take the same number of rounds (the shuffles name all lanes)
-  for (size_t b0 = size_t(blockIdx.x) * (kThreads / 16) + (threadIdx.x >> 5) * 2; b0 < total; b0 += stride) {
-    const size_t b = b0 + ((threadIdx.x >> 4) & 1);
-    const size_t row = b / KB;
-    const int kb = int(b - row * KB);
-    const int col = kb * kFp8Block + sub * 8;
-    const bool in = b < total && col < K;
-    const size_t at = row * size_t(K) + col;
-    float f[8];
-    unpack8<T16>(in ? __ldg(reinterpret_cast<const uint4*>(v + at)) : make_uint4(0, 0, 0, 0), f);
-    float a = amax8(f);
+  for (size_t b0 = size_t(blockIdx.x) * per_cta + (threadIdx.x >> 5) * 2 * kBlocks; b0 < total; b0 += stride) {
+    // the warp's 8 blocks: halves alternate, so that its loads are contiguous
+    uint4 u[kBlocks];
+    size_t at[kBlocks];
+    bool in[kBlocks];
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    const Fp8Scale q = fp8_scale(a);
-    if (in) *reinterpret_cast<uint2*>(codes + at) = quant8(f, q.r);
-    if (b < total && sub == 0) scales[b] = q.s;
+    for (int i = 0; i < kBlocks; ++i) {
+      const size_t b = b0 + 2 * i + (lane >> 4);
+      const size_t row = KB == 1 ? b : b / unsigned(KB);
+      const int col = int(b - row * KB) * kFp8Block + sub * 8;
+      in[i] = b < total && col < K;
+      at[i] = row * size_t(K) + col;
+      u[i] = in[i] ? __ldg(reinterpret_cast<const uint4*>(v + at[i])) : make_uint4(0, 0, 0, 0);
+    }
+    float a[kBlocks];
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      float f[8];
+      unpack8<T16>(u[i], f);
+      a[i] = amax8(f);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) a[i] = fmaxf(a[i], __shfl_xor_sync(0xffffffffu, a[i], o));
+    }
+    const int mine = lane & (kBlocks - 1);
+    const Fp8Scale q = fp8_scale(mine == 0 ? a[0] : mine == 1 ? a[1] : mine == 2 ? a[2] : a[3]);
+    const size_t bm = b0 + 2 * mine + (lane >> 4);
+    if (sub < kBlocks && bm < total) scales[bm] = q.s;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      const float r = __shfl_sync(0xffffffffu, q.r, (lane & 16) + i);
+      float f[8];
+      unpack8<T16>(u[i], f);
+      if (in[i]) *reinterpret_cast<uint2*>(codes + at[i]) = quant8(f, r);
+    }
   }
 }
 
@@ -114,9 +139,11 @@ int quantize_t(const void* v, int batch, int rows, int K, int block_rows, uint8_
   const T16* p = static_cast<const T16*>(v);
   if (block_rows == 1) {
     const size_t all = size_t(batch) * rows;
-    const size_t blocks = (all * fp8_blocks(K) + kThreads / 16 - 1) / (kThreads / 16);
+    const size_t per = kThreads / 16 * kBlocks;
+    const size_t blocks = (all * fp8_blocks(K) + per - 1) / per;
     const size_t most = size_t(num_sms()) * 8 * 8;
-    k_fp8_quant_rows<T16><<<unsigned(blocks < most ? blocks : most), kThreads, 0, stream>>>(p, all, K, codes, scales);
+    MOE_CHECK_CUDA(launch_pdl(k_fp8_quant_rows<T16>, dim3(unsigned(blocks < most ? blocks : most)), dim3(kThreads), 0,
+                              stream, p, all, K, codes, scales));
   } else {
     const size_t blocks = size_t(batch) * fp8_blocks(rows) * fp8_blocks(K);
     MOE_REQUIRE(blocks <= 0x7fffffffu, MOE_ERR_UNSUPPORTED, "moe_fp8_quantize_b128: %zu blocks in one call", blocks);

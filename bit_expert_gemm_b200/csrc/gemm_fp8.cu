@@ -291,6 +291,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&tmem_base_sh, 512);
     tmem_relinquish();
   }
+  // everything above touches no output of the kernel before
+  griddep_wait();
+  griddep_launch_dependents();
   build_tile_table(args, goff, tile_start, warp_sums);
   tc_fence_before();
   __syncthreads();
@@ -633,8 +636,7 @@ int launch(const Args& a, const uint8_t* w, int w_rows, cudaStream_t stream) {
     MOE_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN, SWIGLU>::SMEM_BYTES));
     if (dev < 64) attr_set[dev] = true;
   }
-  kern<<<num_sms(), kThreads, Cfg<BN, SWIGLU>::SMEM_BYTES, stream>>>(ta, tb, to, a);
-  MOE_CHECK_CUDA(cudaGetLastError());
+  MOE_CHECK_CUDA(launch_pdl(kern, dim3(num_sms()), dim3(kThreads), Cfg<BN, SWIGLU>::SMEM_BYTES, stream, ta, tb, to, a));
   return MOE_OK;
 }
 
