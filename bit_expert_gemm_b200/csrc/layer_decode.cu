@@ -219,10 +219,13 @@ inline Layout layout_of(int T, int H, bool f8, size_t stage) {
   l.queue = int((p + 127) / 128 * 128);  // row units keep the 128-byte lines of their swizzle
   return l;
 }
-// Bytes of all selected h rows as phase 2 reads them.
-__host__ __device__ inline size_t h_bytes(int T, int k, int I, bool f8) {
-  const size_t rows = size_t(T) * k;
-  return f8 ? rows * I * 2 + rows * fp8_blocks(I) * 4 : rows * I * 4;
+// The h rows as phase 2 reads them: the routed ones (FP8: and their scales), the shared expert's.
+__host__ __device__ inline int stage_scales(int T, int k, int I) { return T * k * I * 2; }
+__host__ __device__ inline int stage_shared(int T, int k, int I, bool f8) {
+  return f8 ? int(a16(size_t(stage_scales(T, k, I)) + size_t(T) * k * fp8_blocks(I) * 4)) : T * k * I * 4;
+}
+inline size_t stage_bytes(int T, int k, int I, bool f8, bool shared) {
+  return size_t(stage_shared(T, k, I, f8)) + (shared ? size_t(T) * I * 4 : 0);
 }
 
 // E4M3 operands run on the FP16 tensor core: every E4M3 value is an FP16 value
@@ -277,14 +280,14 @@ __device__ __forceinline__ int split_of(int n) {
 // ---------------------------------------------------------------------------
 // phase 0
 // ---------------------------------------------------------------------------
-// Whether FP32 v lies within 8 of its own steps of a rounding border of T16 (or
+// Whether FP32 v lies within 5 of its own steps of a rounding border of T16 (or
 // where FP16 is subnormal): there the FP64 value decides.  The FP32 product
-// below is off by at most 4 steps.
+// below takes four roundings, so it is off by at most 4 of its steps.
 template <typename T16>
 __device__ __forceinline__ bool near_border(float v) {
   const uint32_t u = __float_as_uint(v);
-  if constexpr (std::is_same<T16, __nv_bfloat16>::value) return ((u & 0xffffu) - 0x7ff8u) <= 16u;
-  return ((u & 0x1fffu) - 0x0ff8u) <= 16u || (u & 0x7fffffffu) < 0x38800000u;
+  if constexpr (std::is_same<T16, __nv_bfloat16>::value) return ((u & 0xffffu) - 0x7ffbu) <= 10u;
+  return ((u & 0x1fffu) - 0x0ffbu) <= 10u || (u & 0x7fffffffu) < 0x38800000u;
 }
 template <typename T16>
 __device__ __forceinline__ uint32_t norm_pair(float2 f, float2 w, float r, double rd) {
@@ -333,7 +336,7 @@ __device__ void norm_x(const Args& a, const Smem& s) {
   while ((a.T << lg) > kWarps) --lg;
   const int t = warp >> lg;
   const int nv = a.H / 8;
-  double ss = 0.0;
+  double ss4[4] = {0.0, 0.0, 0.0, 0.0};  // short chains
   if (t < a.T) {
     float lo = 0.0f;
     const uint4* xr = reinterpret_cast<const uint4*>(s.x16() + size_t(t) * x16_pitch(a.H));
@@ -349,14 +352,15 @@ __device__ void norm_x(const Args& a, const Smem& s) {
         const float big = fmaxf(p0, p1), sum = __fadd_rn(p0, p1);
         if (sum < INFINITY) {
           lo += __fsub_rn(fminf(p0, p1), __fsub_rn(sum, big));
-          ss += double(sum);
+          ss4[j] += double(sum);
         } else {  // beyond FP32 (or not finite)
-          ss += double(f.x) * double(f.x) + double(f.y) * double(f.y);
+          ss4[j] += double(f.x) * double(f.x) + double(f.y) * double(f.y);
         }
       }
     }
-    ss += double(lo);
+    ss4[0] += double(lo);
   }
+  double ss = (ss4[0] + ss4[1]) + (ss4[2] + ss4[3]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   if (lane == 0) s.dsum()[warp] = ss;
@@ -957,9 +961,13 @@ struct Down {
       // 16-bit rows are whole 128-byte units (I is a multiple of 64)
       const bool in = wide || iku * 128 + (lane & 7) * 16 < a.I;
       const uint8_t* p = ip + im * 16 * pitch;
-      const bool r0 = in && left > 0, r1 = in && left > 4, r2 = in && left > 8, r3 = in && left > 12;
-      q.push(r0 ? p : a.w_d, r1 ? p + 4 * pitch : a.w_d, r2 ? p + 8 * pitch : a.w_d, r3 ? p + 12 * pitch : a.w_d,
-             r0 ? 16 : 0, r1 ? 16 : 0, r2 ? 16 : 0, r3 ? 16 : 0);
+      // rows past the block's last are not copied: what the slot holds there reaches only results that nobody stores
+      const uint32_t d = q.at(q.in) + q.wr, n = in ? 16 : 0;
+      if (!in) p = ip;
+      if (left > 0) cp_async_16(d, p, n);
+      if (left > 4) cp_async_16(d + 512, p + 4 * pitch, n);
+      if (left > 8) cp_async_16(d + 1024, p + 8 * pitch, n);
+      if (left > 12) cp_async_16(d + 1536, p + 12 * pitch, n);
       if (++im == MT) {
         im = 0;
         ++iu;
@@ -1004,7 +1012,7 @@ struct Down {
     const bool sh = it < 0;
     e.it = it;
     e.n = n;
-    const uint8_t* hb = sh ? static_cast<const uint8_t*>(a.h_sh)
+    const uint8_t* hb = sh ? (a.staged ? s.stage() + stage_shared(a.T, a.k, a.I, F8) : static_cast<const uint8_t*>(a.h_sh))
                            : (a.staged ? s.stage() : (F8 ? reinterpret_cast<const uint8_t*>(a.hq) : static_cast<const uint8_t*>(a.h)));
 #pragma unroll
     for (int x = 0; x < X; ++x) {
@@ -1204,11 +1212,11 @@ struct Down {
   }
 };
 
-// The block's own copy of all 16-bit h rows.
-__device__ void stage_h(const Args& a, const Smem& s) {
-  const uint4* src = static_cast<const uint4*>(a.h);
+// The block's own copy of 16-bit h rows.
+__device__ void stage_h(uint8_t* dst, const void* rows, int bytes) {
+  const uint4* src = static_cast<const uint4*>(rows);
 #pragma unroll 4
-  for (int i = threadIdx.x; i < a.T * a.k * a.I / 4; i += kThreads) reinterpret_cast<uint4*>(s.stage())[i] = __ldcg(src + i);
+  for (int i = threadIdx.x; i < bytes / 16; i += kThreads) reinterpret_cast<uint4*>(dst)[i] = __ldcg(src + i);
 }
 // FP8: quantises (row, 128 features) blocks first, first + step, ... of h, one
 // warp each, four at a time (their loads from L2 together).
@@ -1261,10 +1269,12 @@ __device__ __forceinline__ void columns(const Args& a, const Smem& s, cg::grid_g
   if (F8) cp_async_wait(q.depth - 1);  // the scales; the barriers below come before their use
   if (token) {
     if (a.staged) {
+      if (a.sh_gu) stage_h(s.stage() + stage_shared(a.T, a.k, a.I, F8), a.h_sh, a.T * a.I * 4);
       if (F8)
-        quant_h(a, reinterpret_cast<__half*>(s.stage()), reinterpret_cast<float*>(s.stage() + size_t(a.T) * a.k * a.I * 2), warp, kWarps);
+        quant_h(a, reinterpret_cast<__half*>(s.stage()), reinterpret_cast<float*>(s.stage() + stage_scales(a.T, a.k, a.I)),
+                warp, kWarps);
       else
-        stage_h(a, s);
+        stage_h(s.stage(), a.h, a.T * a.k * a.I * 4);
       __syncthreads();
     } else if (F8) {
       quant_h(a, a.hq, a.hs, blockIdx.x + gridDim.x * warp, gridDim.x * kWarps);
@@ -1401,7 +1411,7 @@ int launch(Args a, cudaStream_t stream) {
   int dev = 0;
   MOE_CHECK_CUDA(cudaGetDevice(&dev));
   MOE_REQUIRE(dev < kMaxDev, MOE_ERR_UNSUPPORTED, "moe_layer_decode: device %d >= %d", dev, kMaxDev);
-  const size_t hb = h_bytes(a.T, a.k, a.I, F8);
+  const size_t hb = stage_bytes(a.T, a.k, a.I, F8, a.sh_gu != nullptr);
   auto room_of = [](size_t fixed) { return fixed < size_t(kSmemMax) ? (kSmemMax - fixed) / kSlotBytes : 0; };
   a.at = layout_of(a.T, a.H, F8, hb);
   a.staged = hb <= size_t(kStageBytes) && room_of(a.at.queue) >= 4;
