@@ -173,7 +173,7 @@ struct Smem {
   const Args& a;
   template <typename V>
   static __device__ __forceinline__ V* at(int off) {
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];
     return reinterpret_cast<V*>(smem + off);
   }
   __device__ __forceinline__ uint8_t* x16() const { return at<uint8_t>(0); }             // [T] rows of x16_pitch bytes
@@ -1406,11 +1406,18 @@ template <typename T16, bool F8, int NT>
 int launch(Args a, cudaStream_t stream) {
   auto kern = k_layer_decode<T16, F8, NT>;
   constexpr int kMaxDev = 64;
-  static size_t smem_set[kMaxDev] = {0};
-  static int co_resident[kMaxDev] = {0};
+  static int blocks[kMaxDev] = {0};
   int dev = 0;
   MOE_CHECK_CUDA(cudaGetDevice(&dev));
   MOE_REQUIRE(dev < kMaxDev, MOE_ERR_UNSUPPORTED, "moe_layer_decode: device %d >= %d", dev, kMaxDev);
+  if (blocks[dev] == 0) {
+    // the largest size once: host threads may come here together
+    MOE_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax));
+    int per_sm = 0;
+    MOE_CHECK_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, kSmemMax));
+    MOE_REQUIRE(per_sm > 0, MOE_ERR_UNSUPPORTED, "moe_layer_decode: kernel does not fit on an SM");
+    blocks[dev] = num_sms();
+  }
   const size_t hb = stage_bytes(a.T, a.k, a.I, F8, a.sh_gu != nullptr);
   auto room_of = [](size_t fixed) { return fixed < size_t(kSmemMax) ? (kSmemMax - fixed) / kSlotBytes : 0; };
   a.at = layout_of(a.T, a.H, F8, hb);
@@ -1421,20 +1428,12 @@ int launch(Args a, cudaStream_t stream) {
   MOE_REQUIRE(room >= 2, MOE_ERR_UNSUPPORTED, "moe_layer_decode: T=%d H=%d do not fit in shared memory", a.T, a.H);
   a.depth = room > size_t(kMaxDepth) ? kMaxDepth : int(room);
   const size_t smem = fixed + size_t(a.depth) * kSlotBytes;
-  if (smem > smem_set[dev]) {
-    MOE_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
-    int per_sm = 0;
-    MOE_CHECK_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem));
-    MOE_REQUIRE(per_sm > 0, MOE_ERR_UNSUPPORTED, "moe_layer_decode: kernel does not fit on an SM");
-    co_resident[dev] = num_sms();
-    smem_set[dev] = smem;
-  }
   a.by_ui = div_magic(a.I / 4);
   a.by_k = div_magic(a.k);
-  a.by_grid = div_magic(co_resident[dev]);
+  a.by_grid = div_magic(blocks[dev]);
   a.by_ib = div_magic(fp8_blocks(a.I));
   void* params[] = {&a};
-  MOE_CHECK_CUDA(cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3(co_resident[dev]), dim3(kThreads),
+  MOE_CHECK_CUDA(cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3(blocks[dev]), dim3(kThreads),
                                              params, smem, stream));
   return MOE_OK;
 }

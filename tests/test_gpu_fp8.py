@@ -296,3 +296,33 @@ def test_refill_and_slice_of_an_fp8_layer():
     ref, r = _layer_ref(small, x, wl.k)
     ok = r["margin"] > 1e-3
     assert rel_err(y.double().cpu().numpy()[ok], ref[ok]) <= 2e-2
+
+
+def test_offsets_past_the_rows_are_cut():
+    T, K, N, E = 5, 128, 64, 2
+    a, sa = abi.moe_fp8_quantize_b128(_values((T, K), 31).to(DEV), 1)
+    w, sw, wd = _bank(E, N, K, seed=3)
+    buf = torch.full((T + 300, N), 3.0, device=DEV)
+    off = torch.tensor([0, 2, 400], dtype=torch.int32, device=DEV)
+    abi.moe_grouped_gemm_fp8_b128(a, sa, w, sw, expert_offsets=off, out=buf[:T])
+    ad, got = fp8.dequant(_np(a), _np(sa)), buf.double().cpu().numpy()
+    assert (got[T:] == 3).all()
+    for lo, hi, e in ((0, 2, 0), (2, 5, 1)):
+        _check(got[lo:hi], ad[lo:hi] @ wd[e].T, np.abs(ad[lo:hi]) @ np.abs(wd[e]).T, K, torch.float32)
+
+
+def test_calls_in_a_row_on_one_workspace():
+    """Back-to-back FFN calls on the same workspace and stream (the kernels overlap
+    their prologues), each read by the next: every result is the first one's."""
+    T, H, I, E, k = 300, 256, 256, 6, 2
+    row_token, off, _ = _routing(T, E, k, seed=41)
+    w = prepare_fp8_weights({"w_gate_up": _values((E, 2 * I, H), 5).to(DEV) * H ** -0.5,
+                             "w_down": _values((E, H, I), 6).to(DEV) * I ** -0.5})
+    args = (w["w8_gu"], w["sc8_gu"], w["w8_d"], w["sc8_d"])
+    ws = abi.workspace(abi.MOE_OP_SWIGLU_FP8_B128, T, H, E, k, I, DEV)
+    xs = [_values((T, H), 50 + i).to(DEV) for i in range(3)]
+    want = [abi.moe_grouped_swiglu_fp8_b128(x, row_token, off, T * k, *args) for x in xs]
+    torch.cuda.synchronize()
+    got = [abi.moe_grouped_swiglu_fp8_b128(xs[i % 3], row_token, off, T * k, *args, ws=ws) for i in range(30)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i % 3]) for i, g in enumerate(got))
