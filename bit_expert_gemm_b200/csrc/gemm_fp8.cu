@@ -204,7 +204,8 @@ struct TileMap {
 // offsets into goff[0..G] (cut to the rows that exist).
 __device__ void build_tile_table(const Args& a, int* goff, int* tile_start, int* warp_sums) {
   const int G = a.G, tid = threadIdx.x;
-  for (int i = tid; i <= G; i += kThreads) goff[i] = a.group_offsets ? min(max(a.group_offsets[i], 0), a.rows) : (i == 0 ? 0 : a.rows);
+  for (int i = tid; i <= G; i += kThreads)
+    goff[i] = a.group_offsets ? min(max(a.group_offsets[i], 0), a.rows) : (i == 0 ? 0 : a.rows);
   __syncthreads();
   const int per = (G + kThreads - 1) / kThreads;
   const int g0 = tid * per;

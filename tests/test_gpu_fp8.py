@@ -326,3 +326,41 @@ def test_calls_in_a_row_on_one_workspace():
     got = [abi.moe_grouped_swiglu_fp8_b128(xs[i % 3], row_token, off, T * k, *args, ws=ws) for i in range(30)]
     torch.cuda.synchronize()
     assert all(torch.equal(g, want[i % 3]) for i, g in enumerate(got))
+
+
+def test_1024_groups_most_of_them_empty():
+    T, K, N, E = 200, 144, 80, 1024
+    w, sw, wd = _bank(E, N, K, seed=5)
+    a, sa = abi.moe_fp8_quantize_b128(_values((T, K), 6).to(DEV), 1)
+    last = np.sort(np.random.default_rng(7).choice(E, 40, replace=False))
+    off = np.searchsorted(last, np.arange(E + 1)) * 5  # five rows for each of the forty
+    assert off[0] == 0 and off[-1] == T and (np.diff(off) > 0).sum() == 40
+    out = abi.moe_grouped_gemm_fp8_b128(a, sa, w, sw, expert_offsets=torch.tensor(off, dtype=torch.int32, device=DEV))
+    ad, got = fp8.dequant(_np(a), _np(sa)), out.double().cpu().numpy()
+    for e in last:
+        lo, hi = off[e], off[e + 1]
+        _check(got[lo:hi], ad[lo:hi] @ wd[e].T, np.abs(ad[lo:hi]) @ np.abs(wd[e]).T, K, out.dtype)
+
+
+def test_more_than_2_to_the_31_elements():
+    """Each row is computed from its own values only, so the rows at the end of a long
+    tensor equal the same rows in a short one."""
+    rows, K = (1 << 20) + 77, 2064
+    tail = _values((300, K), 8).to(DEV)
+    v = torch.zeros((rows, K), dtype=torch.bfloat16, device=DEV)
+    v[-300:] = tail
+    codes, scales = abi.moe_fp8_quantize_b128(v, 1)
+    want = abi.moe_fp8_quantize_b128(tail, 1)
+    assert torch.equal(codes[-300:].view(torch.uint8), want[0].view(torch.uint8))
+    assert torch.equal(scales[-300:], want[1])
+    assert not codes[:-300].view(torch.uint8).any()
+    del v, scales
+    w, sw, _ = _bank(1, 2064, 32, seed=9)
+    a = codes.view(torch.uint8)[:, :32].contiguous()
+    sa = torch.ones((rows, 1), device=DEV)
+    a[-300:] = want[0].view(torch.uint8)[:, :32]
+    for dtype in (torch.bfloat16, torch.float32):
+        small = abi.moe_grouped_gemm_fp8_b128(a[-300:].contiguous(), sa[:300], w, sw, out_dtype=dtype)
+        big = abi.moe_grouped_gemm_fp8_b128(a, sa, w, sw, out_dtype=dtype)
+        assert torch.equal(big[-300:], small) and small.any() and not big[:-300].any()
+        del big

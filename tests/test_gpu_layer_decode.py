@@ -276,3 +276,12 @@ def test_norm_of_large_and_zero_tokens():
     ref, tol, r = _reference(w, x, 2, "bf16", "bf16")
     assert torch.isfinite(y).all()
     _check(y, ref, tol, r)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("T,H,I,E,k,dtype,norm,gate,shared", [
+    (1, 128, 8192, 2, 2, "bf16", False, False, True), (16, 64, 8192, 3, 1, "f16", True, False, True),
+    (16, 64, 64, 1024, 16, "bf16", False, True, True), (4, 4096, 2048, 6, 3, "f16", False, True, True),
+    (8, 4096, 1024, 9, 8, "bf16", True, False, False)])
+def test_layer_at_its_limits(T, H, I, E, k, dtype, norm, gate, shared, fmt):
+    test_layer_against_float64(T, H, I, E, k, dtype, norm, gate, shared, fmt)
