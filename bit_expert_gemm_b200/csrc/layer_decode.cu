@@ -542,6 +542,11 @@ __device__ void shared_gate_value(const Args& a, const Smem& s) {
 // shuffles (about 600 cycles at E = 512 against 2500 for k rounds of two warp
 // reductions).  More than 32 at the bound (ties): the rounds.
 // ---------------------------------------------------------------------------
+// The rounds, out of line: the way there is rare, and code that is stepped over has
+// to be fetched.
+__device__ __noinline__ void select_rounds(const float* row, int E, int k, int lane, int* idx_out, float* w_out) {
+  topk_token<32>(row, E, k, k, lane, idx_out, w_out, nullptr);
+}
 template <int NV>
 __device__ void select_token(const float* row, int E, int k, int lane, int* idx_out, float* w_out, uint32_t* buf) {
   uint32_t key[NV], best = 0;
@@ -576,7 +581,7 @@ __device__ void select_token(const float* row, int E, int k, int lane, int* idx_
   }
   __syncwarp();
   if (n > 32) {
-    topk_token<NV>(row, E, k, k, lane, idx_out, w_out, nullptr);
+    select_rounds(row, E, k, lane, idx_out, w_out);
     return;
   }
   const uint32_t my = lane < n ? buf[lane] : 0u;
@@ -764,7 +769,7 @@ struct GateUp {
       const uint8_t *ga = pa + (in ? iu * 128 : 0), *gb = pb + (in ? iu * 128 : 0);
       q.push(ga, gb, ga + up, gb + up, na, nb, na, nb);
       iu += 1 << ir.lg;
-      if (iu >= KU) {
+      if (__builtin_expect(iu >= KU, 0)) {
         next(ir);
         enter();
       }
@@ -958,7 +963,7 @@ struct Down {
         im = 0;
         ++iu;
         ip += 128;
-        if (++iku == ilen) {
+        if (__builtin_expect(++iku == ilen, 0)) {
           iku = 0;
           ++iit;
           if (iu < u1) rows_of();
@@ -1184,12 +1189,11 @@ __device__ void quant_h(const Args& a, __half* codes, float* scales, int first, 
   }
 }
 
-// Columns [n0, n0 + nrows) of y; in the first call the rest of barrier 2 and
-// the h rows' way into the operand form come between the requests and the
-// products.
+// Columns [n0, n0 + nrows) of y, at most 16 MT; the rest of barrier 2 and the h
+// rows' way into the operand form come between the requests and the products.
 template <typename T16, bool F8, int MT, int NT>
 __device__ __forceinline__ void columns(const Args& a, const Smem& s, cg::grid_group& grid,
-                                        cg::grid_group::arrival_token* token, int nd, int n0, int nrows) {
+                                        cg::grid_group::arrival_token&& token, int nd, int n0, int nrows) {
   const int warp = threadIdx.x >> 5;
   // nobody reads x any more: the warps' sums [16][T][16 MT] end where red ends, the queue takes what is before them
   uint8_t* const end = reinterpret_cast<uint8_t*>(s.red()) + kRedBytes;
@@ -1199,15 +1203,12 @@ __device__ __forceinline__ void columns(const Args& a, const Smem& s, cg::grid_g
   for (int i = threadIdx.x; i < bytes / 4; i += kThreads) ysum[i] = 0.0f;
   Down<T16, F8, MT, NT> down(a, s, q, ysum + warp * a.T * 16 * MT, nd, n0, nrows);
   down.start();
-  if (token) grid.barrier_wait(std::move(*token));
-  if (F8 && token) {
-    if (a.staged) {
-      quant_h(a, reinterpret_cast<__half*>(s.stage()), reinterpret_cast<float*>(s.stage() + stage_scales(a.T, a.k, a.I)),
-              warp, kWarps);
-    } else {
-      quant_h(a, a.hq, a.hs, blockIdx.x + gridDim.x * warp, gridDim.x * kWarps);
-      grid.sync();
-    }
+  grid.barrier_wait(std::move(token));
+  if (F8) {
+    __half* const codes = a.staged ? reinterpret_cast<__half*>(s.stage()) : a.hq;
+    float* const scales = a.staged ? reinterpret_cast<float*>(s.stage() + stage_scales(a.T, a.k, a.I)) : a.hs;
+    quant_h(a, codes, scales, a.staged ? warp : blockIdx.x + gridDim.x * warp, a.staged ? kWarps : gridDim.x * kWarps);
+    if (!a.staged) grid.sync();
   }
   __syncthreads();  // the sums are zero, the codes written
   down.run();
@@ -1227,7 +1228,7 @@ __device__ __forceinline__ void columns(const Args& a, const Smem& s, cg::grid_g
   __syncthreads();
 }
 
-template <typename T16, bool F8, int NT>
+template <typename T16, bool F8, int NT, int MT>
 __global__ void __launch_bounds__(kThreads, 1) k_layer_decode(const Args a) {
   cg::grid_group grid = cg::this_grid();
   const Smem s{a};
@@ -1312,21 +1313,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_layer_decode(const Args a) {
   }
   auto token2 = grid.barrier_arrive();
 
-  // ---- phase 2: down and the weighted sum, up to 32 columns at a time
+  // ---- phase 2: down and the weighted sum
   const int2 col = share_of(a.H, a.by_grid);
-  if (col.y - col.x <= 16) {
-    columns<T16, F8, 1, NT>(a, s, grid, &token2, nd, col.x, col.y - col.x);
-  } else {
-    columns<T16, F8, 2, NT>(a, s, grid, &token2, nd, col.x, min(32, col.y - col.x));
-#pragma unroll 1
-    for (int n0 = col.x + 32; n0 < col.y; n0 += 32)
-      columns<T16, F8, 2, NT>(a, s, grid, nullptr, nd, n0, min(32, col.y - n0));
-  }
+  columns<T16, F8, MT, NT>(a, s, grid, std::move(token2), nd, col.x, col.y - col.x);
 }
 
-template <typename T16, bool F8, int NT>
+template <typename T16, bool F8, int NT, int MT>
 int launch(Args a, cudaStream_t stream) {
-  auto kern = k_layer_decode<T16, F8, NT>;
+  auto kern = k_layer_decode<T16, F8, NT, MT>;
   constexpr int kMaxDev = 64;
   static int blocks[kMaxDev] = {0};
   int dev = 0;
@@ -1340,6 +1334,7 @@ int launch(Args a, cudaStream_t stream) {
     MOE_REQUIRE(per_sm > 0, MOE_ERR_UNSUPPORTED, "moe_layer_decode: kernel does not fit on an SM");
     blocks[dev] = num_sms();
   }
+  MOE_REQUIRE(a.H <= 16 * MT * blocks[dev], MOE_ERR_UNSUPPORTED, "moe_layer_decode: H=%d on %d SMs", a.H, blocks[dev]);
   const size_t hb = F8 ? stage_bytes(a.T, a.k, a.I) : 0;
   auto room_of = [](size_t fixed) { return fixed < size_t(kSmemMax) ? (kSmemMax - fixed) / kSlotBytes : 0; };
   a.at = layout_of(a.T, a.H, F8, hb);
@@ -1360,12 +1355,18 @@ int launch(Args a, cudaStream_t stream) {
   return MOE_OK;
 }
 
+template <typename T16, bool F8, int NT>
+int launch_mt(const Args& a, cudaStream_t stream) {
+  // one 16-row tile where a block's columns fit in it: a second, empty one costs 2 to 10
+  // us (BF16 T = 1 30.7 against 32.9, FP8 T = 8 63 against 74)
+  return a.H <= 16 * num_sms() ? launch<T16, F8, NT, 1>(a, stream) : launch<T16, F8, NT, 2>(a, stream);
+}
 template <typename T16>
 int dispatch(const Args& a, bool f8, cudaStream_t stream) {
   // FP8 up to 8 tokens: one 8-token operand in place of two (57 against 62 us at T = 8);
   // with 16-bit weights the second one costs nothing that could be measured
-  if (f8) return a.T <= 8 ? launch<T16, true, 1>(a, stream) : launch<T16, true, 2>(a, stream);
-  return launch<T16, false, 2>(a, stream);
+  if (f8) return a.T <= 8 ? launch_mt<T16, true, 1>(a, stream) : launch_mt<T16, true, 2>(a, stream);
+  return launch_mt<T16, false, 2>(a, stream);
 }
 
 }  // namespace
