@@ -3,7 +3,9 @@
 //
 // Bound by HBM: 2 bytes in, 1 out per element, the scales are 1/32 or 1/4096
 // of that.  The block is held in registers between the maximum and the
-// codes, so it is read once.
+// codes, so it is read once.  Measured: 8192 x 2048 BF16 by rows 12.4 us (launch
+// included; 4.1 TB/s), 64 x 1280 x 2048 by 128 x 128 blocks 93 us (5.4 TB/s of
+// the 6.45 of a copy).
 #include "fp8.cuh"
 
 namespace moe {

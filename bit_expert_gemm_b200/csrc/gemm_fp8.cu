@@ -27,6 +27,13 @@
 // products 545; 1 owns the TMEM), 3 scales (row scale x column block scale of every
 // step into shared memory, ahead of the promotion warps), 4..7 A-row gather, 8..15 promotion
 // and epilogue (two per 32 rows, each half of the tile's columns).
+//
+// Measured: 8192 x 4096 x 2048 in 84 us in a burst (1650 TFLOP/s), 95 under load;
+// 163840 rows x 2048 x 640 in 256 groups 353 and 420; the FFN of 8192 tokens, 512
+// experts, k = 10, H = 2048, I = 640 602 and 720.  A step's operands pass shared
+// memory twice (48 KB written, 48 KB read: 750 cycles against 512 of products);
+// promotion and the output's way add the rest (without them 57 us of the 86, without
+// the products too 45).
 #include "fp8.cuh"
 #include "gemm_sm100.cuh"
 
@@ -664,7 +671,10 @@ int grouped_gemm_fp8(const uint8_t* a, const float* a_scales, int a_rows, const 
   g.a_rows = a_rows;
   g.status = device_status_ptr();
   g.limit_ns = wait_limit_ns();
-  // the wide tile where an upper bound of its tiles still covers the SMs
+  // the wide tile where an upper bound of its tiles still covers the SMs: it reads the
+  // A operand half as often (8192 x 4096 x 2048 in 83 us against 96, 163840 rows of 256
+  // groups 353 against 436); fewer tiles than SMs leave some of them idle (640 rows of
+  // 512 groups: 105 against 106 us, even)
   const long mt = (rows + BM - 1) / BM + (E < rows ? E : rows);
   if (mt * ((N + 255) / 256) >= num_sms()) return launch<256, false>(g, w, E * N, stream);
   return launch<128, false>(g, w, E * N, stream);
