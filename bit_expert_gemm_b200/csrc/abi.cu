@@ -722,6 +722,7 @@ static int layer_decode_entry(const char* fn, const void* x, int T, int H, const
   MOE_REQUIRE(T >= 0 && H > 0 && I > 0 && E >= 1 && k >= 1, MOE_ERR_INVALID_ARG,
               "%s: bad sizes T=%d H=%d I=%d E=%d k=%d", fn, T, H, I, E, k);
   MOE_REQUIRE(dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F16, MOE_ERR_INVALID_ARG, "%s: dtype %d", fn, dtype);
+  MOE_REQUIRE(!norm_w || eps >= 0.0f, MOE_ERR_INVALID_ARG, "%s: eps must be >= 0", fn);
   MOE_REQUIRE(k <= 16 && k <= E && E <= 1024, MOE_ERR_UNSUPPORTED, "%s: need k <= 16, k <= E <= 1024 (k=%d E=%d)", fn, k,
               E);
   MOE_REQUIRE(H % 64 == 0 && I % 64 == 0 && I <= 8192 && layer_decode_fits(T, H), MOE_ERR_UNSUPPORTED,

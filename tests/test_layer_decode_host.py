@@ -71,3 +71,12 @@ def test_binding_refusals():
 
     with pytest.raises(ValueError, match="fused_decode"):
         MoELayer({"w_router": r, "w_sh_down": d[0], "w_gu": d, "bias": None}, 2, fmt="nvfp4", T_max=1, fused_decode=True)
+
+
+def test_negative_or_nan_eps_is_refused():
+    b, b2 = P(256), P(1 << 20)
+    for eps in (-1.0, float("nan")):
+        rc = _code("moe_layer_decode_bf16", b, 4, 128, b, eps, None, b, None, 8, 2, 64, b, b, None, None, 0, None, None,
+                   b2, b, 1 << 24, None)
+        assert rc == abi.MOE_ERR_INVALID_ARG
+        assert "eps" in abi.load().moe_last_error().decode()
