@@ -30,13 +30,13 @@
 // bytes of a weight row are a lane's fragment.  The copies (cp.async, whole
 // 128-byte lines) go to a queue of each warp in shared memory: no other warp
 // reads it, so there is no block barrier on the way, the queue can be indexed
-// at run time, and 2 to 8 units a warp (what x leaves of the 227 KB, 32 KB a unit
-// of all warps; from 5 on the time is the same) are in flight.  A few tokens leave
-// the tensor core idle most of the time; what counts is the stream: tcgen05 would want the
-// weights as whole 128-row tiles and its result back from TMEM, for products
-// that already fit in a few registers.  (A ring of registers in place of the
-// queue: 44 / 258 / 52 / 103 us on the four layers below; a queue of each lane
-// with 64-byte pieces: 38 / 171 / 39 / 84.)
+// at run time, and 2 to 5 units a warp (what x leaves of the 227 KB, 32 KB a unit
+// of all warps; 8 took as long) are in flight.  A few tokens leave the tensor core
+// idle most of the time; what counts is the stream: tcgen05 would want the weights
+// as whole 128-row tiles and its result back from TMEM, for products that already
+// fit in a few registers.  (A ring of registers in place of the queue: 44 / 258 /
+// 52 / 103 us on the four layers below; a queue of each lane with 64-byte pieces:
+// 38 / 171 / 39 / 84.)
 //
 // Measured (I = 640, k = 10, shared expert, bias; CUDA events, weights not in L2):
 //   BF16 T = 1,  H = 2048, E = 512               88.6 MB   29.2 us
@@ -47,6 +47,8 @@
 // down, whose rows are short, at 1.5 to 4; at T = 1 a layer with next to no weights
 // takes 15 us: x and the norm 2, the router 2, each grid barrier 1.5 to 2, the
 // selection 2.5.  The four-launch form of the same BF16 layer takes 41 us at T = 1.
+// A fifth of the warps' time goes to instruction fetch, so the loops are kept short:
+// unrolled twice, gate/up costs 1 us at T = 1 and down 1 to 8.
 //
 // Every sum is FP32 in an order fixed by the sizes (the router's in FP64 over
 // pieces of 32 products, so that the selection does not hang on the order of
@@ -79,7 +81,7 @@ constexpr int kMaxSlots = 16;               // selected experts per token
 constexpr int kMaxList = kLayerDecodeMaxT * kMaxSlots;
 constexpr int kUnitBytes = 16 * 128;        // a row unit
 constexpr int kSlotBytes = kWarps * kUnitBytes;
-constexpr int kMaxDepth = 8;
+constexpr int kMaxDepth = 5;
 // FP8: up to this size every block quantises all of h for itself, into shared
 // memory, which saves a grid barrier.
 // At T = 1 (13 KB) 27.4 us against 28.8 with the barrier; at T = 2 (26 KB) the two are
@@ -115,7 +117,7 @@ struct Args {
   __half* hq;             // FP8, not staged: h's codes as FP16 values in operand order [T * k, I], and their scales
   float* hs;
   int staged;             // FP8: every block keeps h's codes in shared memory
-  int depth;              // queue slots per lane, 2 .. kMaxDepth
+  int depth;              // queue slots per warp, 2 .. kMaxDepth
   // multipliers of div_small for the divisors I/4, k, the grid and the 128-feature blocks of I
   uint32_t by_ui, by_k, by_grid, by_ib;
   Layout at;
@@ -143,19 +145,11 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait_n() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void cp_async_wait(int pending) {  // 1 .. 7
-  if (pending >= 4) {
-    if (pending >= 6) {
-      if (pending == 6) cp_async_wait_n<6>(); else cp_async_wait_n<7>();
-    } else {
-      if (pending == 4) cp_async_wait_n<4>(); else cp_async_wait_n<5>();
-    }
+__device__ __forceinline__ void cp_async_wait(int pending) {  // 1 .. kMaxDepth - 1
+  if (pending >= 3) {
+    if (pending == 3) cp_async_wait_n<3>(); else cp_async_wait_n<4>();
   } else {
-    if (pending >= 2) {
-      if (pending == 2) cp_async_wait_n<2>(); else cp_async_wait_n<3>();
-    } else {
-      cp_async_wait_n<1>();
-    }
+    if (pending == 2) cp_async_wait_n<2>(); else cp_async_wait_n<1>();
   }
 }
 
