@@ -463,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row_in_tile = q * 32 + lane;
     int buf = 0;
     uint32_t buf_phase = 0, x_phase = 0;
+    uint32_t box_no = 0;  // 16-bit output: this warp's boxes, over all tiles
     bool ok = true;
     for (int L = blockIdx.x; L < total && ok; L += gridDim.x) {
       const TileMap t = decode_tile(L, nt, tile_start, G);
@@ -568,12 +569,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           // boxes of 32 rows x 64 columns: written to shared memory in the 128-byte
           // swizzle and copied out by the tensor copy unit (whole lines, and the warp
           // goes on), or by the warp where rows are missing (they belong to the next
-          // group)
+          // group).  A warp's two boxes take turns over all its tiles, not within one: a
+          // half of a tile may hold a single box (BN = 128, or the last columns), and the
+          // one copy that may still be reading has to be the other box's.
           auto store16 = [&](auto pack) {
 #pragma unroll
             for (int c = 0; c < NC / 64; ++c) {
               if (col0 + 64 * c >= args.n_out) break;
-              uint8_t* box = stg_w + (c & 1) * kBoxBytes;
+              uint8_t* box = stg_w + (box_no & 1) * kBoxBytes;
+              ++box_no;
               if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the copy before last has read
               __syncwarp();
 #pragma unroll
