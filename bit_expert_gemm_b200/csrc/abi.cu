@@ -77,7 +77,7 @@ int grouped_swiglu_fp8(const void* x, const int32_t* row_token, const int32_t* o
                        int E, const uint8_t* w_gu, const float* sc_gu, const uint8_t* w_d, const float* sc_d,
                        int dtype, int out_fp32, void* f, void* ws, size_t ws_bytes, cudaStream_t stream);
 size_t layer_decode_ws_bytes(int T, int E, int k, int I);
-bool layer_decode_fits(int T, int H);
+bool layer_decode_fits(int T, int H, int E, int k, int I);
 int layer_decode(const void* x, int T, int H, const void* norm_w, float eps, const void* w_shared_gate,
                  const void* w_router, const float* bias, int E, int k, int I, const void* w_gu, const float* sc_gu,
                  const void* w_d, const float* sc_d, bool f8, const void* w_sh_gu, const void* w_sh_d, int dtype,
@@ -335,7 +335,7 @@ size_t moe_workspace_size(int op, int T, int H, int E, int k_slots, int I) {
     case MOE_OP_SWIGLU_NVFP4: return nvfp4_ws_bytes(rows, H, I, E);
     case MOE_OP_REFILL: return refill_ws_bytes(T, k_slots > 0 ? k_slots - 1 : 0);
     case MOE_OP_NVFP4_QUANTIZE: return nvfp4_quant_ws_bytes(1, T, H);
-    case MOE_OP_LAYER_DECODE: return layer_decode_fits(T, H) ? layer_decode_ws_bytes(T, E, k_slots, I) : 0;
+    case MOE_OP_LAYER_DECODE: return layer_decode_fits(T, H, E, k_slots, I) ? layer_decode_ws_bytes(T, E, k_slots, I) : 0;
     case MOE_OP_SWIGLU_FP8_B128: return fp8_swiglu_ws_bytes(T, rows, H, I);
     default: return 0;
   }
@@ -723,10 +723,9 @@ static int layer_decode_entry(const char* fn, const void* x, int T, int H, const
               "%s: bad sizes T=%d H=%d I=%d E=%d k=%d", fn, T, H, I, E, k);
   MOE_REQUIRE(dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F16, MOE_ERR_INVALID_ARG, "%s: dtype %d", fn, dtype);
   MOE_REQUIRE(!norm_w || eps >= 0.0f, MOE_ERR_INVALID_ARG, "%s: eps must be >= 0", fn);
-  MOE_REQUIRE(k <= 16 && k <= E && E <= 1024, MOE_ERR_UNSUPPORTED, "%s: need k <= 16, k <= E <= 1024 (k=%d E=%d)", fn, k,
-              E);
-  MOE_REQUIRE(H % 64 == 0 && I % 64 == 0 && I <= 8192 && layer_decode_fits(T, H), MOE_ERR_UNSUPPORTED,
-              "%s: need T <= 16, H %% 64 == 0, H <= 4096, T * H <= 40960, I %% 64 == 0 (T=%d H=%d I=%d)", fn, T, H, I);
+  MOE_REQUIRE(layer_decode_fits(T, H, E, k, I), MOE_ERR_UNSUPPORTED,
+              "%s: need T <= 16, H %% 64 == 0, H <= 4096, H <= 32 * SMs, T * H <= 40960, I %% 64 == 0, I <= 8192, k <= 16, "
+              "k <= E <= 1024 (T=%d H=%d I=%d k=%d E=%d)", fn, T, H, I, k, E);
   if (T == 0) return MOE_OK;
   MOE_REQUIRE(x && w_router && w_gu && w_d && y && ws && (!f8 || (sc_gu && sc_d)), MOE_ERR_INVALID_ARG,
               "%s: null pointer", fn);

@@ -72,6 +72,8 @@ namespace moe {
 constexpr int kLayerDecodeMaxT = 16;
 constexpr int kLayerDecodeMaxH = 4096;
 constexpr int kLayerDecodeMaxTH = 40960;  // T * H: x (and its codes) in shared memory
+constexpr int kLayerDecodeMaxI = 8192;
+constexpr int kLayerDecodeMaxE = 1024;
 
 namespace {
 
@@ -1328,7 +1330,6 @@ int launch(Args a, cudaStream_t stream) {
     MOE_REQUIRE(per_sm > 0, MOE_ERR_UNSUPPORTED, "moe_layer_decode: kernel does not fit on an SM");
     blocks[dev] = num_sms();
   }
-  MOE_REQUIRE(a.H <= 16 * MT * blocks[dev], MOE_ERR_UNSUPPORTED, "moe_layer_decode: H=%d on %d SMs", a.H, blocks[dev]);
   const size_t hb = F8 ? stage_bytes(a.T, a.k, a.I) : 0;
   auto room_of = [](size_t fixed) { return fixed < size_t(kSmemMax) ? (kSmemMax - fixed) / kSlotBytes : 0; };
   a.at = layout_of(a.T, a.H, F8, hb);
@@ -1365,8 +1366,12 @@ int dispatch(const Args& a, bool f8, cudaStream_t stream) {
 
 }  // namespace
 
-bool layer_decode_fits(int T, int H) {
-  return T <= kLayerDecodeMaxT && H <= kLayerDecodeMaxH && T * H <= kLayerDecodeMaxTH;
+// The sizes that the kernel takes: everything else is refused, and has no workspace size.
+// A block holds at most two 16-row tiles of output columns, so H is also bounded by the SMs.
+bool layer_decode_fits(int T, int H, int E, int k, int I) {
+  return T >= 0 && T <= kLayerDecodeMaxT && H > 0 && H % 64 == 0 && H <= kLayerDecodeMaxH && T * H <= kLayerDecodeMaxTH &&
+         I > 0 && I % 64 == 0 && I <= kLayerDecodeMaxI && k >= 1 && k <= kMaxSlots && k <= E && E <= kLayerDecodeMaxE &&
+         H <= 32 * num_sms();
 }
 
 size_t layer_decode_ws_bytes(int T, int E, int k, int I) {

@@ -121,7 +121,8 @@ MOE_API int moe_selftest_bounded_wait(int limit_us, int32_t* result, void* strea
 
 /* Bytes of workspace that operation `op` needs for the given sizes
  * (T tokens, hidden size H, E experts, k_slots selected slots per token,
- * intermediate width I).  Returns 0 for an unknown op.  The result is an
+ * intermediate width I).  Returns 0 for an unknown op, and for
+ * MOE_OP_LAYER_DECODE for sizes that its calls refuse.  The result is an
  * upper bound valid for any routing of those sizes. */
 MOE_API size_t moe_workspace_size(int op, int T, int H, int E, int k_slots, int I);
 
@@ -536,9 +537,9 @@ MOE_API int moe_grouped_swiglu_fp8_b128(const void* x, const int32_t* row_token,
  * [2I, H] and w_sh_down [H, I], or both NULL; topk_idx [T, k] int32 and topk_w
  * [T, k] FP32, or NULL.
  * One cooperative launch over all SMs: calls on different streams run one
- * after the other.  Limits: T <= 16, H % 64 == 0, H <= 4096, T * H <= 40960,
- * I % 64 == 0, I <= 8192, 1 <= k <= 16, k <= E <= 1024; x, y and all weights
- * 16-byte aligned.
+ * after the other.  Limits: T <= 16, H % 64 == 0, H <= 4096, H <= 32 * SMs of
+ * the device, T * H <= 40960, I % 64 == 0, I <= 8192, 1 <= k <= 16, k <= E <=
+ * 1024; x, y and all weights 16-byte aligned.
  * Workspace: MOE_OP_LAYER_DECODE (k_slots = k), not shared with a call that
  * may run at the same time.
  * ------------------------------------------------------------------------- */
