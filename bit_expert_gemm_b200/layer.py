@@ -152,7 +152,9 @@ class MoELayer:
         # route + permute in one call; the T_max workspace covers every T <= T_max
         self.ws_route = abi.workspace(abi.MOE_OP_ROUTE_PERMUTE, T_max, H, E, ks, 0, d)
         self.ws_ffn = abi.workspace(op, T_max, H, E, ks, self.I, d)
-        self.ws_sh = abi.workspace(abi.MOE_OP_SWIGLU_BF16, T_max, H, 1, 1, self.I_sh, d)
+        # the shared expert's small-batch form (T <= 16) may need more than T_max tokens' h
+        need_sh = max(abi.moe_workspace_size(abi.MOE_OP_SWIGLU_BF16, t, H, 1, 1, self.I_sh) for t in {T_max, min(T_max, 16)})
+        self.ws_sh = torch.empty(max(256, need_sh), dtype=torch.uint8, device=d)
         # decode-sized batches run a separate shared expert (the library's
         # weight-streaming GEMVs for one dense expert) on a second stream
         self._sh_stream = T_max <= 16
