@@ -531,11 +531,11 @@ MOE_API int moe_grouped_swiglu_fp8_b128(const void* x, const int32_t* row_token,
  * The router's logits are summed in FP64, so a near-tie resolves by the exact
  * logits rounded to FP32; NaN logits rank last; a token needs at least one
  * finite logit for its weights to be numbers.
- * x, y [T, H] dtype (y must not overlap x); norm_w [H] or NULL; w_shared_gate
- * [H] or NULL (needs the shared expert); w_router [E, H]; bias [E] FP32 or
- * NULL; expert weights and scales as in the calls named above; w_sh_gate_up
- * [2I, H] and w_sh_down [H, I], or both NULL; topk_idx [T, k] int32 and topk_w
- * [T, k] FP32, or NULL.
+ * x, y [T, H] dtype (y may be x, but not overlap it in part); norm_w [H] or
+ * NULL; w_shared_gate [H] or NULL (needs the shared expert); w_router [E, H];
+ * bias [E] FP32 or NULL; expert weights and scales as in the calls named
+ * above; w_sh_gate_up [2I, H] and w_sh_down [H, I], or both NULL; topk_idx
+ * [T, k] int32 and topk_w [T, k] FP32, or NULL.
  * One cooperative launch over all SMs: calls on different streams run one
  * after the other.  Limits: T <= 16, H % 64 == 0, H <= 4096, H <= 32 * SMs of
  * the device, T * H <= 40960, I % 64 == 0, I <= 8192, 1 <= k <= 16, k <= E <=

@@ -1,6 +1,6 @@
 """The one-kernel decode layer's limits, without a GPU: the workspace size is 0
-for exactly the sizes that the calls refuse, and MoELayer leaves those to the
-chain of calls."""
+for exactly the sizes that the calls refuse, MoELayer leaves those to the chain
+of calls, and the output may take the input's place."""
 
 import ctypes
 
@@ -36,3 +36,13 @@ def test_layers_outside_the_limits_keep_the_chain(I, sizes):
          "w_sh_down": torch.zeros((H, I), dtype=torch.bfloat16),
          "w8_gu": torch.zeros((E, 2 * I, H), dtype=torch.uint8), "w8_d": torch.zeros((E, H, I), dtype=torch.uint8)}
     assert sorted(MoELayer(w, 2, fmt="fp8_b128", T_max=20).decode_ws) == sizes
+
+
+def test_y_may_be_x_but_not_a_part_of_it():
+    def call(y):  # no workspace bytes: the last check before a launch refuses
+        return abi.load().moe_layer_decode_bf16(P(4096), 4, 256, None, ctypes.c_float(1e-6), None, P(4096), None, 16, 2,
+                                                64, P(4096), P(4096), None, None, 0, None, None, P(y), P(4096), 0, None)
+
+    nb = 4 * 256 * 2
+    assert call(4096) == call(4096 + nb) == call(4096 - nb) == abi.MOE_ERR_WORKSPACE
+    assert call(4096 + 512) == call(4096 + nb - 16) == call(4096 - 512) == abi.MOE_ERR_INVALID_ARG
