@@ -293,10 +293,12 @@ __device__ __forceinline__ bool near_border(float v) {
   if constexpr (std::is_same<T16, __nv_bfloat16>::value) return ((u & 0xffffu) - 0x7ffbu) <= 10u;
   return ((u & 0x1fffu) - 0x0ffbu) <= 10u || (u & 0x7fffffffu) < 0x38800000u;
 }
+// far: r itself left FP32's normal range (tokens of about 2^126 and more, or with a
+// norm below 2^-128: both need BF16).
 template <typename T16>
-__device__ __forceinline__ uint32_t norm_pair(float2 f, float2 w, float r, double rd) {
+__device__ __forceinline__ uint32_t norm_pair(float2 f, float2 w, float r, double rd, bool far) {
   const float a = f.x * r * (1.0f + w.x), b = f.y * r * (1.0f + w.y);
-  if (near_border<T16>(a) || near_border<T16>(b)) {
+  if (far || near_border<T16>(a) || near_border<T16>(b)) {
     const double ad = double(f.x) * rd * (1.0 + double(w.x)), bd = double(f.y) * rd * (1.0 + double(w.y));
     T16 o[2];
     if constexpr (std::is_same<T16, __nv_bfloat16>::value) {
@@ -333,6 +335,7 @@ __device__ void fetch_x(const Args& a, const Smem& s) {
 // RMSNorm of the rows in place: 16 / T' warps per token (T' the power of two at
 // or above T) add the squares, then every thread scales one chunk of columns of
 // every token.
+constexpr float kSquareMin = 7.8886090522101181e-31f;  // 2^-100
 template <typename T16>
 __device__ void norm_x(const Args& a, const Smem& s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -348,16 +351,17 @@ __device__ void norm_x(const Args& a, const Smem& s) {
     for (int c = (warp & ((1 << lg) - 1)) * 32 + lane; c < nv; c += 32 << lg) {
       const uint4 v = xr[c];
       const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-      // squares are exact in FP32; a pair's sum is taken with its rounding error
+      // A square of at least 2^-126 is exact in FP32 (16 bits at most), and a smaller one beside
+      // a sum of 2^-100 or more is off by 2^-50 of it; the sum is taken with its rounding error.
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 f = Pack2<T16>::unpack(u[j]);
         const float p0 = f.x * f.x, p1 = f.y * f.y;
         const float big = fmaxf(p0, p1), sum = __fadd_rn(p0, p1);
-        if (sum < INFINITY) {
+        if (sum >= kSquareMin && sum < INFINITY) {
           lo += __fsub_rn(fminf(p0, p1), __fsub_rn(sum, big));
           ss4[j] += double(sum);
-        } else {  // beyond FP32 (or not finite)
+        } else {  // squares rounded or lost in FP32, beyond it, or not finite
           ss4[j] += double(f.x) * double(f.x) + double(f.y) * double(f.y);
         }
       }
@@ -390,12 +394,13 @@ __device__ void norm_x(const Args& a, const Smem& s) {
     if (i >= a.T) break;
     const double rd = reinterpret_cast<const double*>(s.sel_idx())[i];
     const float r = float(rd);
+    const bool far = !(r >= FLT_MIN && r < INFINITY);
     uint4* at = reinterpret_cast<uint4*>(s.x16() + size_t(i) * x16_pitch(a.H)) + c;
     const uint4 v = *at, w = reinterpret_cast<const uint4*>(norm_w_of(s))[c];
     const uint32_t u[4] = {v.x, v.y, v.z, v.w}, g[4] = {w.x, w.y, w.z, w.w};
     uint32_t o[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = norm_pair<T16>(Pack2<T16>::unpack(u[j]), Pack2<T16>::unpack(g[j]), r, rd);
+    for (int j = 0; j < 4; ++j) o[j] = norm_pair<T16>(Pack2<T16>::unpack(u[j]), Pack2<T16>::unpack(g[j]), r, rd, far);
     *at = make_uint4(o[0], o[1], o[2], o[3]);
   }
   __syncthreads();

@@ -6,8 +6,11 @@ import pytest
 import torch
 
 from bit_expert_gemm_b200 import MoELayer, abi
-from tests.helpers import rel_err
+from bit_expert_gemm_b200.layer import prepare_fp8_weights
+from oracle import moe
+from tests.helpers import f64, rel_err
 from tests.test_gpu_fp8 import _layer_case, _layer_ref
+from tests.test_gpu_layer_decode import DEV, _call, _case
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +51,21 @@ def test_layer_on_its_own_output(T, fmt):
         want = chain.forward(layer.y[1:T].clone()).clone()
         assert torch.equal(layer.forward(layer.y[1:T]), want)
     assert abi.moe_device_status() == 0
+
+
+def test_norm_of_tiny_and_huge_tokens_without_eps():
+    """eps = 0 is allowed: tokens whose squares, or whose reciprocal norm, leave
+    FP32's range are normalised from FP64 all the same.  x_norm is pinned bit for
+    bit: the layer on it, without its norm, gives the same y."""
+    H, k = 512, 3
+    w, x = _case(8, H, 64, 24, k, seed=41, norm=True)
+    scale = [1.0, 2.0 ** -70, 2.0 ** -100, 2.0 ** -129, 2.0 ** 60, 2.0 ** 126, 2.0 ** -63, 1.0]
+    x = (x.double().clamp(-3.9, 3.9) * torch.tensor(scale, device=DEV, dtype=torch.float64)[:, None]).to(x.dtype)
+    x[6, ::2] = 0
+    x[7, 3:] *= 2.0 ** -90  # three features set the norm, the others all but vanish
+    xn = torch.from_numpy(moe.block_input(f64(x), f64(w["w_norm"]), eps=0.0)).to(x.dtype).to(DEV)
+    assert torch.isfinite(xn).all() and (xn != 0).any(1).all()
+    for fmt in ("bf16", "fp8"):
+        w = prepare_fp8_weights(w)
+        plain = {n: v for n, v in w.items() if n != "w_norm"}
+        assert torch.equal(_call(w, x, k, fmt, eps=0.0), _call(plain, xn, k, fmt))
