@@ -54,6 +54,11 @@ constexpr int kThreads = 512;
 constexpr int kGatherWarp0 = 4;
 constexpr int kEpiWarp0 = 8;
 constexpr int kSmemBudget = 212 * 1024;
+// In place of the scale of a row without a token: a NaN that no product gives (those are
+// 0x7fffffff), by which the epilogue finds the row.  The SwiGLU form takes 0 there, which
+// makes the row zero for finite weights: the check would cost it registers (732 against
+// 717 us on 8192 tokens), and its rows are promised no more.
+constexpr uint32_t kNoRow = 0xffc0ffeeu;
 constexpr int kStoreStride = 64 + 16;  // output staging: bytes per row of a 64-byte chunk, padded
 constexpr int kBoxBytes = 32 * 128;    // 16-bit output: a box of 32 rows x 64 columns, two per warp
 // registers per thread of the role groups: the sum over the four groups of
@@ -379,11 +384,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const TileMap t = decode_tile(L, nt, tile_start, G);
         const int row0 = goff[t.g] + t.m * BM;
         const int tile_rows = min(BM, min(goff[t.g + 1], args.rows) - row0);
-        int src[4];  // scale rows of tile rows lane, lane + 32, ..; -1: no row
+        int src[4];      // scale rows of tile rows lane, lane + 32, ..; -1: none
+        float none[4];  // their scale: 0 past the tile's rows, which nobody stores
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = lane + 32 * i;
           int v = r < tile_rows ? row0 + r : -1;
+          none[i] = !SWIGLU && v >= 0 ? __uint_as_float(kNoRow) : 0.0f;
           if (gathered && v >= 0) v = __ldg(args.row_token + v);
           src[i] = v >= 0 && v < args.a_rows ? v : -1;
         }
@@ -405,8 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!mbar_poll(&tempty_bar[buf], buf_phase ^ 1, &abort_flag, status, lim)) { ok = false; break; }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            step_scale[buf][0][lane + 32 * i] = a[i] * w0;
-            step_scale[buf][1][lane + 32 * i] = a[i] * w1;
+            step_scale[buf][0][lane + 32 * i] = src[i] >= 0 ? a[i] * w0 : none[i];
+            step_scale[buf][1][lane + 32 * i] = src[i] >= 0 ? a[i] * w1 : none[i];
             a[i] = na[i];
           }
           w0 = nw0;
@@ -470,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tile_rows = min(BM, min(goff[t.g + 1], args.rows) - (goff[t.g] + t.m * BM));
       const size_t out_row = size_t(goff[t.g]) + size_t(t.m) * BM + row_in_tile;
       const bool valid = row_in_tile < tile_rows;
+      uint32_t row_scale = 0;
       // columns of this thread: output columns col0 .. (SwiGLU: BNH/2 of them, gate and up)
       const int col0 = t.n * BNH + half * (SWIGLU ? BNH / 2 : NC);
       const bool live = q * 32 < tile_rows && col0 < args.n_out;  // uniform in the warp
@@ -483,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (live) {
           const uint32_t s0 = __float_as_uint(step_scale[buf][SWIGLU ? 0 : half][row_in_tile]);
+          if (!SWIGLU) row_scale = s0;
           const uint32_t s1 = SWIGLU ? __float_as_uint(step_scale[buf][1][row_in_tile]) : s0;
           const uint64_t p0 = pack2(s0, s0), p1 = pack2(s1, s1);
           // SwiGLU: the first half of the chunks are gate columns, the rest the matching up columns
@@ -520,6 +529,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++buf == NACC) { buf = 0; buf_phase ^= 1; }
       }
       if (!ok) break;
+      if (!SWIGLU && row_scale == kNoRow)  // zero, where a weight or its scale is not finite too
+#pragma unroll
+        for (int i = 0; i < NC / 2; ++i) acc[i] = 0;
       uint8_t* stg_w = smem + STAGES * C::STAGE_BYTES + (warp - kEpiWarp0) * (SWIGLU ? 32 * kStoreStride : 2 * kBoxBytes);
       const int nvalid = tile_rows - q * 32;  // rows of this warp that exist
       const size_t row0 = size_t(goff[t.g]) + size_t(t.m) * BM + q * 32;

@@ -507,7 +507,9 @@ MOE_API int moe_grouped_gemm_fp8_b128(const uint8_t* a, const float* a_scales, c
  *   ceil(H/128)] FP32 (gate and up are separate tensors: their blocks do not
  *   mix); w_d [E, H, I], sc_d [E, ceil(H/128), ceil(I/128)].
  * x [T, H] dtype; row_token [rows] or NULL (rows == T); expert_offsets [E+1];
- * f [rows, H], FP32 when out_fp32 != 0, else dtype.
+ * f [rows, H], FP32 when out_fp32 != 0, else dtype.  A row whose row_token
+ * lies outside [0, T) is zero where its expert's weights are finite; rows from
+ * expert_offsets[E] on are left as they were.
  * Limits: H % 64 == 0, I % 64 == 0, E <= 1024, E * max(2I, H) < 2^31;
  * operands 16-byte aligned.  Workspace: MOE_OP_SWIGLU_FP8_B128 (the codes and
  * scales of x and h).

@@ -1,11 +1,12 @@
 """The FP8 grouped product on the GPU where its tiles meet: several tiles per
-thread block, halves of a tile with a single box of 16-bit output columns.
-Tolerances as in test_gpu_fp8."""
+thread block, halves of a tile with a single box of 16-bit output columns, and
+rows without a token beside weights that are not finite.  Tolerances as in test_gpu_fp8."""
 
 import pytest
 import torch
 
 from bit_expert_gemm_b200 import abi
+from bit_expert_gemm_b200.layer import prepare_fp8_weights
 from oracle import fp8
 from tests.test_gpu_fp8 import DEV, HALF, U, _np, _values
 
@@ -38,4 +39,45 @@ def test_several_tiles_per_block(rows, N, K, dtype):
         for out in outs[3 * i:3 * i + 3]:
             bad = (out.double() - ref).abs() > tol
             assert not bad.any(), int(bad.sum())
+    assert abi.moe_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_without_a_token_are_zero_beside_bad_weights(dtype):
+    """Rows whose row_token is out of range are zero where the expert's weights hold
+    a NaN code or an infinite scale; rows with a token show them."""
+    T, K, N, E = 9, 272, 144, 2
+    a, sa = abi.moe_fp8_quantize_b128(_values((T, K), 1).to(DEV), 1)
+    wv = _values((E, N, K), 2, spread=0.3)
+    wv[0, 3, 5], wv[0, 130, 200], wv[1, 7, 260] = float("nan"), float("inf"), float("-inf")
+    w, sw = abi.moe_fp8_quantize_b128(wv.to(DEV), 128)
+    row_token = torch.tensor([0, -1, 4, T, 8, -2 ** 31, 2 ** 31 - 1, 3], dtype=torch.int32, device=DEV)
+    off = torch.tensor([0, 4, 8], dtype=torch.int32, device=DEV)
+    out = abi.moe_grouped_gemm_fp8_b128(a, sa, w, sw, expert_offsets=off, row_token=row_token, out_dtype=dtype)
+    gone = (row_token < 0) | (row_token >= T)
+    assert (out[gone] == 0).all()
+    bad = torch.zeros((2, N), dtype=torch.bool, device=DEV)
+    bad[0, 3] = True
+    bad[0, 128:] = True  # the scale of rows 128.. and columns 128..255
+    bad[1, :128] = True  # the scale of rows ..127 and columns 256..
+    want = bad[[0, 0, 1, 1]]
+    assert torch.equal(torch.isfinite(out[~gone]), ~want)
+    assert abi.moe_device_status() == 0
+
+
+def test_expert_rows_without_a_token_and_behind_the_last():
+    T, H, I, E = 9, 192, 128, 2
+    w = prepare_fp8_weights({"w_gate_up": _values((E, 2 * I, H), 5).to(DEV) * H ** -0.5,
+                             "w_down": _values((E, H, I), 6).to(DEV) * I ** -0.5})
+    args = (w["w8_gu"], w["sc8_gu"], w["w8_d"], w["sc8_d"])
+    x = _values((T, H), 4).to(DEV)
+    row_token = torch.tensor([0, -1, 4, T, 8, 2 ** 31 - 1, 3, 1, 1], dtype=torch.int32, device=DEV)
+    off = torch.tensor([0, 4, 7], dtype=torch.int32, device=DEV)
+    f = torch.full((9, H), 7.0, dtype=torch.bfloat16, device=DEV)
+    abi.moe_grouped_swiglu_fp8_b128(x, row_token, off, 9, *args, f=f)
+    assert (f[7:] == 7).all() and (f[[1, 3, 5]] == 0).all()
+    # the other rows are those of a batch without the absent ones
+    some = torch.tensor([0, 2, 4, 6], device=DEV)
+    off2 = torch.tensor([0, 2, 4], dtype=torch.int32, device=DEV)
+    assert torch.equal(f[some], abi.moe_grouped_swiglu_fp8_b128(x, row_token[some].contiguous(), off2, 4, *args))
     assert abi.moe_device_status() == 0
