@@ -136,6 +136,8 @@ MOE_API size_t moe_workspace_size(int op, int T, int H, int E, int k_slots, int 
  *              (the expert Refill-RMS promotes [RAZOR]).
  *   topk_w   = softmax(l)[S] / sum softmax(l)[S]  (sums to 1 over the k slots)
  *
+ * A NaN logit counts as the lowest finite FP32 number: it ranks above -inf and
+ * ties with a mask of that number by index.
  * x [T, H] and w_router [E, H] are 16-bit (dtype); bias [E] FP32 or NULL.
  * Outputs: topk_idx [T, k+extra] int32, topk_w [T, k] FP32, topk_logit
  * [T, k+extra] FP32 (the logits l of the selected experts, bias included; may
@@ -531,8 +533,8 @@ MOE_API int moe_grouped_swiglu_fp8_b128(const void* x, const int32_t* row_token,
  * moe_grouped_swiglu_fp8_b128: x_norm and h quantised per 128 features); the
  * router and the shared expert stay of `dtype`.
  * The router's logits are summed in FP64, so a near-tie resolves by the exact
- * logits rounded to FP32; NaN logits rank last; a token needs at least one
- * finite logit for its weights to be numbers.
+ * logits rounded to FP32; NaN logits count as in moe_route_topk; a token needs
+ * at least one finite logit for its weights to be numbers.
  * x, y [T, H] dtype (y may be x, but not overlap it in part); norm_w [H] or
  * NULL; w_shared_gate [H] or NULL (needs the shared expert); w_router [E, H];
  * bias [E] FP32 or NULL; expert weights and scales as in the calls named

@@ -69,3 +69,32 @@ def test_norm_of_tiny_and_huge_tokens_without_eps():
         w = prepare_fp8_weights(w)
         plain = {n: v for n, v in w.items() if n != "w_norm"}
         assert torch.equal(_call(w, x, k, fmt, eps=0.0), _call(plain, xn, k, fmt))
+
+
+@pytest.mark.parametrize("E", [24, 200, 900])
+def test_selection_among_nan_and_masked_logits(E):
+    """A NaN logit counts as the lowest finite number, as in moe_route_topk: behind
+    every finite logit above it, tied by index with that mask, before -inf.  With
+    the many ties of E = 200 and 900 the selection goes by rounds."""
+    T, H, I, low = 5, 192, 64, torch.finfo(torch.float32).min
+    w, x = _case(T, H, I, E, 2, seed=E)
+    bias = torch.full((E,), float("-inf"), device=DEV)
+    bias[[4, 17]] = 0.0
+    bias[9] = float("nan")
+    bias[[7, 20]] = low
+    if E > 24:
+        bias[24:] = low
+    w["bias"] = bias
+    want = {2: [4, 17], 3: [4, 17, 7], 4: [4, 17, 7, 9], 5: [4, 17, 7, 9, 20]}
+    if E == 24:  # two more than are left: the first of the -inf ones
+        want[7] = [4, 17, 7, 9, 20, 0, 1]
+    for k, order in want.items():
+        idx, tw = torch.empty((T, k), dtype=torch.int32, device=DEV), torch.empty((T, k), device=DEV)
+        y = _call(w, x, k, "bf16", topk_idx=idx, topk_w=tw)
+        ridx, rw, _ = abi.moe_route_topk(x, w["w_router"], bias, k)
+        assert torch.equal(idx, ridx)
+        assert (idx[:, :2].sort(1).values == torch.tensor([4, 17], device=DEV)).all()
+        assert (idx[:, 2:].cpu() == torch.tensor(order[2:], dtype=torch.int32)).all()
+        assert (tw[:, 2:] == 0).all() and (tw[:, :2].sum(1) - 1).abs().max() <= 2.0 ** -21
+        # the chain's logits: H FP32 additions, each off by 2^-24 of sum |x w| <= 16; half of that in a weight of two
+        assert (tw - rw).abs().max() <= H * 2.0 ** -24 * 16 / 2 and torch.isfinite(y).all()
