@@ -50,10 +50,11 @@
 // A fifth of the warps' time goes to instruction fetch, so the loops are kept short:
 // unrolled twice, gate/up costs 1 us at T = 1 and down 1 to 8.
 //
-// Every sum is FP32 in an order fixed by the sizes (the router's in FP64 over
-// pieces of 32 products, so that the selection does not hang on the order of
-// summation); x_norm is rounded to 16 bits from a value accurate beyond FP32
-// for the same reason.  For 16-bit weights h is kept as the sum of two 16-bit
+// Every sum is FP32 in an order fixed by the sizes.  The router adds its pieces of
+// 32 products (one FP32 sum of the tensor core each: 32 additions, off by at most
+// 2^-18 of the terms' magnitudes) in FP64, so the error of a logit does not grow
+// with H; x_norm is rounded to 16 bits from a value accurate beyond FP32, since
+// the selection depends on it.  For 16-bit weights h is kept as the sum of two 16-bit
 // numbers (the tensor core's operand type; hi + lo holds it to 2^-16 of its
 // value in BF16, so y carries one 16-bit rounding, not two: one rounded h had
 // 1.4 to 1.55 times the error); FP8 experts quantise h from FP32.

@@ -532,9 +532,11 @@ MOE_API int moe_grouped_swiglu_fp8_b128(const void* x, const int32_t* row_token,
  * moe_experts_bf16; h is rounded to dtype).  _fp8_b128: FP8 experts (as
  * moe_grouped_swiglu_fp8_b128: x_norm and h quantised per 128 features); the
  * router and the shared expert stay of `dtype`.
- * The router's logits are summed in FP64, so a near-tie resolves by the exact
- * logits rounded to FP32; NaN logits count as in moe_route_topk; a token needs
- * at least one finite logit for its weights to be numbers.
+ * The router's products are summed in FP32 by the tensor core over pieces of
+ * 32 features and in FP64 over the pieces: a logit is within 2^-18 sum |x w| of
+ * the exact one before it is rounded to FP32, and logits closer than that may
+ * rank either way.  NaN logits count as in moe_route_topk; a token needs at
+ * least one finite logit for its weights to be numbers.
  * x, y [T, H] dtype (y may be x, but not overlap it in part); norm_w [H] or
  * NULL; w_shared_gate [H] or NULL (needs the shared expert); w_router [E, H];
  * bias [E] FP32 or NULL; expert weights and scales as in the calls named

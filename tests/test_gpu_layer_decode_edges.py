@@ -98,3 +98,26 @@ def test_selection_among_nan_and_masked_logits(E):
         assert (tw[:, 2:] == 0).all() and (tw[:, :2].sum(1) - 1).abs().max() <= 2.0 ** -21
         # the chain's logits: H FP32 additions, each off by 2^-24 of sum |x w| <= 16; half of that in a weight of two
         assert (tw - rw).abs().max() <= H * 2.0 ** -24 * 16 / 2 and torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("H", [64, 512, 4096])
+def test_selection_at_the_stated_accuracy_of_the_logits(H, dtype):
+    """Logits that differ by little more than twice the stated bound, 2^-18 sum |x w|
+    and the rounding to FP32, are ranked as the exact ones.  The bias puts the
+    exact logits on such a ladder (its own rounding to FP32 is part of them)."""
+    E, k = 40, 16
+    for seed in range(6):
+        w, x = _case(1, H, 64, E, k, dtype, seed=100 * seed + H)
+        terms = f64(w["w_router"]) * f64(x)
+        dot, mag = terms.sum(1), np.abs(terms).sum(1).max()
+        place = np.random.RandomState(seed).permutation(E)
+        bound = 2.0 ** -18 * mag + 2.0 ** -24
+        ladder = 0.5 - 2.5 * bound * place
+        w["bias"] = torch.from_numpy((ladder - dot).astype(np.float32)).to(DEV)
+        exact = dot + w["bias"].double().cpu().numpy()
+        order = np.argsort(-exact, kind="stable")
+        assert np.abs(exact).max() < 1 and np.diff(-exact[order]).min() > 2 * bound
+        idx = torch.empty((1, k), dtype=torch.int32, device=DEV)
+        _call(w, x, k, "bf16", topk_idx=idx)
+        assert idx[0].tolist() == order[:k].tolist()
