@@ -56,7 +56,7 @@
 // with H; x_norm is rounded to 16 bits from a value accurate beyond FP32, since
 // the selection depends on it.  For 16-bit weights h is kept as the sum of two 16-bit
 // numbers (the tensor core's operand type; hi + lo holds it to 2^-16 of its
-// value in BF16, so y carries one 16-bit rounding, not two: one rounded h had
+// value in BF16, 2^-22 or 2^-25 in FP16, so y carries one 16-bit rounding, not two: one rounded h had
 // 1.4 to 1.55 times the error); FP8 experts quantise h from FP32.
 #include <cooperative_groups.h>
 

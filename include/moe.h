@@ -529,9 +529,12 @@ MOE_API int moe_grouped_swiglu_fp8_b128(const void* x, const int32_t* row_token,
  * its optional gate sigmoid(x_norm . w_shared_gate), and
  *   y[t] = sum_j topk_w[t, j] * f_j(x_norm[t]) (+ gate[t] * shared(x_norm[t]))
  * summed in FP32 and rounded once to dtype.  _bf16: experts of `dtype` (as
- * moe_experts_bf16; h is rounded to dtype).  _fp8_b128: FP8 experts (as
- * moe_grouped_swiglu_fp8_b128: x_norm and h quantised per 128 features); the
- * router and the shared expert stay of `dtype`.
+ * moe_experts_bf16, but h is not rounded to dtype: it is held as the sum of two
+ * such numbers, to 2^-16 of its value in BF16, in FP16 to 2^-22 or 2^-25,
+ * whichever is larger; an FP16 h of 65520 or more is infinite).  _fp8_b128: FP8
+ * experts (as moe_grouped_swiglu_fp8_b128: x_norm and h quantised per 128
+ * features); the router and the shared expert (its h held in two numbers too)
+ * stay of `dtype`.
  * The router's products are summed in FP32 by the tensor core over pieces of
  * 32 features and in FP64 over the pieces: a logit is within 2^-18 sum |x w| of
  * the exact one before it is rounded to FP32, and logits closer than that may

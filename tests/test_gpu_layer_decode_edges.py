@@ -9,7 +9,7 @@ from bit_expert_gemm_b200 import MoELayer, abi
 from bit_expert_gemm_b200.layer import prepare_fp8_weights
 from oracle import moe
 from tests.helpers import f64, rel_err
-from tests.test_gpu_fp8 import _layer_case, _layer_ref
+from tests.test_gpu_fp8 import HALF, U, _layer_case, _layer_ref
 from tests.test_gpu_layer_decode import DEV, _call, _case
 
 pytestmark = pytest.mark.gpu
@@ -121,3 +121,46 @@ def test_selection_at_the_stated_accuracy_of_the_logits(H, dtype):
         idx = torch.empty((1, k), dtype=torch.int32, device=DEV)
         _call(w, x, k, "bf16", topk_idx=idx)
         assert idx[0].tolist() == order[:k].tolist()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_h_is_held_in_two_numbers(dtype):
+    """Down rows that take the difference of two nearly equal features of h: with h
+    rounded once to 16 bits they would be off by 2^-8 (BF16) of it.  The bound is the
+    header's for h, the FP32 sums' and y's own rounding."""
+    T, H, I = 4, 128, 64
+    w, x = _case(T, H, I, 1, 1, dtype, seed=51)
+    gu = w["w_gate_up"][0]
+    gu[1:I:2] = gu[0:I:2]              # gate features in equal pairs
+    gu[I + 1::2] = gu[I::2]            # up features too,
+    gu[I + 1::2, 5] *= 1 + 2.0 ** -5   # but for one weight
+    wd = torch.zeros_like(w["w_down"][0])
+    pairs = torch.arange(H, device=DEV) % (I // 2)
+    wd[torch.arange(H), 2 * pairs], wd[torch.arange(H), 2 * pairs + 1] = 1.0, -1.0
+    w["w_down"][0] = wd
+    y = f64(_call(w, x, 1, "bf16", shared=False))
+    x64, wg, wu, wd = f64(x), f64(gu[:I]), f64(gu[I:]), f64(wd)
+    g, u = x64 @ wg.T, x64 @ wu.T
+    dg, du = (H + 3) * U * (np.abs(x64) @ np.abs(wg).T), (H + 3) * U * (np.abs(x64) @ np.abs(wu).T)
+    h = moe.silu(g) * u
+    dh = 1.1 * dg * np.abs(u) + (np.abs(moe.silu(g)) + 1.1 * dg) * du + 16 * U * np.abs(h)
+    held = 2.0 ** -16 * np.abs(h) if dtype == "bf16" else np.maximum(2.0 ** -22 * np.abs(h), 2.0 ** -25)
+    ref = h @ wd.T
+    tol = (dh + held + 3 * U * np.abs(h)) @ np.abs(wd).T
+    tol = tol + HALF[x.dtype] * (np.abs(ref) + tol) + (2.0 ** -25 if dtype == "f16" else 0.0)
+    assert (np.abs(y - ref) <= tol).all()
+    once = f64(torch.from_numpy(h).to(x.dtype)) @ wd.T
+    assert (np.abs(once - ref) > tol).any()  # the test tells the two apart
+
+
+def test_an_fp16_h_beyond_its_range_is_infinite():
+    T, H, I = 2, 64, 64
+    w, x = _case(T, H, I, 1, 1, "f16", seed=52)
+    x[1, 0] = 16.0
+    w["w_gate_up"][0][:, 0] = 0.0
+    w["w_gate_up"][0][0, 0] = w["w_gate_up"][0][I, 0] = 20.0  # g and u of feature 0: about 320 for token 1
+    w["w_down"][0][:, 0] = torch.where(torch.arange(H, device=DEV) % 2 == 0, 0.5, -0.5).half()
+    x[0, 0] = 0.0
+    y = _call(w, x, 1, "bf16", shared=False)
+    assert torch.isfinite(y[0]).all()
+    assert (y[1, 0::2] == float("inf")).all() and (y[1, 1::2] == float("-inf")).all()
