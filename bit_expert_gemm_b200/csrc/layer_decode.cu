@@ -50,7 +50,10 @@
 // A fifth of the warps' time goes to instruction fetch, so the loops are kept short:
 // unrolled twice, gate/up costs 1 us at T = 1 and down 1 to 8.
 //
-// Every sum is FP32 in an order fixed by the sizes.  The router adds its pieces of
+// Every sum is FP32.  The same call gives the same bits; the order of a token's
+// sums depends on the sizes and on how many distinct experts the batch selects
+// (how many warps share a group of gate/up units, where the warps' runs of down
+// units are cut), so its last bits may change with the other tokens.  The router adds its pieces of
 // 32 products (one FP32 sum of the tensor core each: 32 additions, off by at most
 // 2^-18 of the terms' magnitudes) in FP64, so the error of a logit does not grow
 // with H; x_norm is rounded to 16 bits from a value accurate beyond FP32, since

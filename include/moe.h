@@ -545,6 +545,9 @@ MOE_API int moe_grouped_swiglu_fp8_b128(const void* x, const int32_t* row_token,
  * bias [E] FP32 or NULL; expert weights and scales as in the calls named
  * above; w_sh_gate_up [2I, H] and w_sh_down [H, I], or both NULL; topk_idx
  * [T, k] int32 and topk_w [T, k] FP32, or NULL.
+ * The same call gives the same bits.  The order of a token's sums depends on
+ * the number of distinct experts that the batch selects, so its last bits may
+ * change with the other tokens of the batch.
  * One cooperative launch over all SMs: calls on different streams run one
  * after the other.  Limits: T <= 16, H % 64 == 0, H <= 4096, H <= 32 * SMs of
  * the device, T * H <= 40960, I % 64 == 0, I <= 8192, 1 <= k <= 16, k <= E <=

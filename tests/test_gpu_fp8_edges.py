@@ -8,7 +8,7 @@ import torch
 from bit_expert_gemm_b200 import abi
 from bit_expert_gemm_b200.layer import prepare_fp8_weights
 from oracle import fp8
-from tests.test_gpu_fp8 import DEV, HALF, U, _np, _values
+from tests.test_gpu_fp8 import DEV, HALF, U, _np, _routing, _values
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +81,18 @@ def test_expert_rows_without_a_token_and_behind_the_last():
     off2 = torch.tensor([0, 2, 4], dtype=torch.int32, device=DEV)
     assert torch.equal(f[some], abi.moe_grouped_swiglu_fp8_b128(x, row_token[some].contiguous(), off2, 4, *args))
     assert abi.moe_device_status() == 0
+
+
+def test_expert_rows_whatever_the_workspace_holds():
+    T, H, I, E, k = 50, 256, 192, 6, 2
+    w = prepare_fp8_weights({"w_gate_up": _values((E, 2 * I, H), 5).to(DEV) * H ** -0.5,
+                             "w_down": _values((E, H, I), 6).to(DEV) * I ** -0.5})
+    args = (w["w8_gu"], w["sc8_gu"], w["w8_d"], w["sc8_d"])
+    x = _values((T, H), 4).to(DEV)
+    row_token, off, _ = _routing(T, E, k, seed=3)
+    want = abi.moe_grouped_swiglu_fp8_b128(x, row_token, off, T * k, *args)
+    assert torch.isfinite(want).all()
+    ws = abi.workspace(abi.MOE_OP_SWIGLU_FP8_B128, T, H, E, k, I, DEV)
+    for fill in (0xff, 0x00, 0x7f):
+        ws.fill_(fill)
+        assert torch.equal(abi.moe_grouped_swiglu_fp8_b128(x, row_token, off, T * k, *args, ws=ws), want)

@@ -10,7 +10,7 @@ from bit_expert_gemm_b200.layer import prepare_fp8_weights
 from oracle import moe
 from tests.helpers import f64, rel_err
 from tests.test_gpu_fp8 import HALF, U, _layer_case, _layer_ref
-from tests.test_gpu_layer_decode import DEV, _call, _case
+from tests.test_gpu_layer_decode import DEV, _call, _case, _check, _reference
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +164,22 @@ def test_an_fp16_h_beyond_its_range_is_infinite():
     y = _call(w, x, 1, "bf16", shared=False)
     assert torch.isfinite(y[0]).all()
     assert (y[1, 0::2] == float("inf")).all() and (y[1, 1::2] == float("-inf")).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_same_bits_whatever_the_workspace_holds(fmt):
+    """Repeated calls give the same bits, on a workspace of NaNs and after a larger
+    batch; a token among others stays within the roundings of its own sums."""
+    T, k = 12, 3
+    w, x = _case(T, 512, 192, 40, k, seed=61, norm=True, gate=True)
+    w = prepare_fp8_weights(w)
+    ws = abi.workspace(abi.MOE_OP_LAYER_DECODE, T, 512, 40, k, 192, DEV)
+    for t in (1, 3, T):
+        want = _call(w, x[:t], k, fmt)
+        for fill in (0xff, 0x00, 0x7f):
+            ws.fill_(fill)
+            assert torch.equal(_call(w, x[:t], k, fmt, ws=ws), want)
+        _call(w, x, k, fmt, ws=ws)
+        assert torch.equal(_call(w, x[:t], k, fmt, ws=ws), want)
+        ref, tol, r = _reference(w, x[:t], k, fmt, "bf16")
+        _check(want, ref, tol, r)
