@@ -96,3 +96,43 @@ def test_expert_rows_whatever_the_workspace_holds():
     for fill in (0xff, 0x00, 0x7f):
         ws.fill_(fill)
         assert torch.equal(abi.moe_grouped_swiglu_fp8_b128(x, row_token, off, T * k, *args, ws=ws), want)
+
+
+def test_quantiser_and_product_captured_on_a_given_stream():
+    """A graph of the quantiser and the gathered product replayed with other values
+    and other rows, and the same two calls on a stream that is passed."""
+    T, K, N, E = 70, 272, 192, 3
+    w, sw = abi.moe_fp8_quantize_b128(_values((E, N, K), 2, spread=0.3).to(DEV), 128)
+    rows = [_routing(T, E, 2, seed=s)[:2] for s in (1, 2)]
+    xs = [_values((T, K), 10 + s).to(DEV) for s in (1, 2)]
+
+    def calls(x, row_token, off, codes, scales, out, stream=None):
+        abi.moe_fp8_quantize_b128(x, 1, codes=codes, scales=scales, stream=stream)
+        abi.moe_grouped_gemm_fp8_b128(codes, scales, w, sw, expert_offsets=off, row_token=row_token, out=out,
+                                      stream=stream)
+
+    def buffers():
+        return (torch.empty((T, K), dtype=torch.float8_e4m3fn, device=DEV), torch.empty((T, 3), device=DEV),
+                torch.empty((2 * T, N), dtype=torch.float16, device=DEV))
+
+    want = []
+    for x, (rt, off) in zip(xs, rows):
+        b = buffers()
+        calls(x, rt, off, *b)
+        want.append(b[2])
+    x, rt, off, b = xs[0].clone(), rows[0][0].clone(), rows[0][1].clone(), buffers()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls(x, rt, off, *b)
+    for i in (1, 0, 1):
+        x.copy_(xs[i])
+        rt.copy_(rows[i][0])
+        off.copy_(rows[i][1])
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(b[2], want[i])
+    s, b2 = torch.cuda.Stream(), buffers()
+    torch.cuda.synchronize()
+    calls(xs[0], *rows[0], *b2, stream=s)
+    s.synchronize()
+    assert torch.equal(b2[2], want[0])

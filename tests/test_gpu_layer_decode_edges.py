@@ -183,3 +183,34 @@ def test_same_bits_whatever_the_workspace_holds(fmt):
         assert torch.equal(_call(w, x[:t], k, fmt, ws=ws), want)
         ref, tol, r = _reference(w, x[:t], k, fmt, "bf16")
         _check(want, ref, tol, r)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_two_host_threads_and_a_given_stream(fmt):
+    """Calls from two host threads, each on the stream that it passes."""
+    import threading
+
+    k = 3
+    w, x = _case(8, 256, 128, 16, k, seed=71, norm=True)
+    w = prepare_fp8_weights(w)
+    parts = [x[:3].contiguous(), x[3:].contiguous()]
+    want = [_call(w, p, k, fmt) for p in parts]
+    outs = [[torch.empty_like(p) for _ in range(20)] for p in parts]
+    wss = [abi.workspace(abi.MOE_OP_LAYER_DECODE, 8, 256, 16, k, 128, DEV) for _ in parts]
+    streams = [torch.cuda.Stream() for _ in parts]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            for y in outs[i]:
+                _call(w, parts[i], k, fmt, y=y, ws=wss[i], stream=streams[i])
+        except Exception as e:  # reported by the test's own thread
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    assert not failed
+    assert all(torch.equal(y, want[i]) for i in range(2) for y in outs[i])
