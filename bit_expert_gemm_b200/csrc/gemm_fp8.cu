@@ -28,12 +28,14 @@
 // step into shared memory, ahead of the promotion warps), 4..7 A-row gather, 8..15 promotion
 // and epilogue (two per 32 rows, each half of the tile's columns).
 //
-// Measured: 8192 x 4096 x 2048 in 84 us in a burst (1650 TFLOP/s), 95 under load;
-// 163840 rows x 2048 x 640 in 256 groups 353 and 420; the FFN of 8192 tokens, 512
-// experts, k = 10, H = 2048, I = 640 602 and 720.  A step's operands pass shared
-// memory twice (48 KB written, 48 KB read: 750 cycles against 512 of products);
-// promotion and the output's way add the rest (without them 57 us of the 86, without
-// the products too 45).
+// Measured: 8192 x 4096 x 2048 in 84 us in a burst (1650 TFLOP/s), 96 under load;
+// 163840 rows x 2048 x 640 in 256 groups 353 and 425; the FFN of 8192 tokens, 512
+// experts, k = 10, H = 2048, I = 640 602 and 729.  A K step takes 1320 cycles, its
+// products 512, and no unit is busy half of the time (tensor pipe 38 %, packed FMAs
+// 49 %, the products' operand reads 29 %): with two accumulators the order of a
+// step's parts sets the pace.  Left out in copies of the dense product's 86.5 us:
+// promotion and the output's way 57, the products too 45, the hand-overs too 40,
+// which is the operands' way from L2 (48 KB a step in 590 cycles).
 #include "fp8.cuh"
 #include "gemm_sm100.cuh"
 

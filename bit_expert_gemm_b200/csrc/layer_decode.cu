@@ -39,10 +39,10 @@
 // 38 / 171 / 39 / 84.)
 //
 // Measured (I = 640, k = 10, shared expert, bias; CUDA events, weights not in L2):
-//   BF16 T = 1,  H = 2048, E = 512               88.6 MB   29.2 us
-//   FP16 T = 16, H = 2560, E = 256, norm, gate    444 MB    115 us (3.9 of 6.45 TB/s)
+//   BF16 T = 1,  H = 2048, E = 512               88.6 MB   29.1 us
+//   FP16 T = 16, H = 2560, E = 256, norm, gate    444 MB    116 to 125 us by selection (3.8 of 6.45 TB/s)
 //   FP8  T = 1,  H = 2048, E = 512               49.3 MB   26.7 us
-//   FP8  T = 8,  H = 2048, E = 512, norm, gate    152 MB   53.3 us
+//   FP8  T = 8,  H = 2048, E = 512, norm, gate    152 MB   55.9 us
 // While weights stream, gate/up runs at 3.4 (FP8, T = 1) to 6 TB/s (T = 16) and
 // down, whose rows are short, at 1.5 to 4; at T = 1 a layer with next to no weights
 // takes 15 us: x and the norm 2, the router 2, each grid barrier 1.5 to 2, the

@@ -17,8 +17,10 @@ refill_pass(x, stats)    one Refill-RMS scoring pass (k+1 slots), adds to the
                          statistics and returns y
 fused_decode=True        (the default for "fp8_b128", also for "bf16") runs
                          forward on at most 16 tokens as one kernel
-                         (moe_layer_decode_*) where its limits allow; the
-                         "bf16" default keeps the chain of calls
+                         (moe_layer_decode_*) where its limits allow, else as
+                         the chain of calls.  The "bf16" default keeps the
+                         chain (T = 1: 40.5 against 29.5 us, T = 16: 137.5
+                         against 131.9), whose roundings its users have
 capture(x, fn)           records one pass (forward, or any callable over the
                          layer's buffers) into a CUDA graph bound to the
                          device buffer x; replaying the graph re-runs the
